@@ -26,7 +26,13 @@ EXPORTS = (
     "hisa_last_cuda_error", "hisa_version", "hisa_token_topk_noalloc", "hisa_forward_cached", "hisa_gather_probe",
     "hisa_block_candidates_workspace_size", "hisa_block_candidates", "hisa_topk_merge", "hisa_remap_ids",
     "hisa_lse_merge", "hisa_forward_host_workspace_size", "hisa_forward_host", "hisa_sparse_attn_kernel",
+    "hisa_tree_attn_workspace_size", "hisa_tree_attn_fwd", "hisa_cache_weight_workspace_size", "hisa_cache_weight",
+    "hisa_cache_keep_workspace_size", "hisa_cache_keep", "hisa_cache_compact",
 )
+
+MAX_DRAFT = 256       # slots for drafted tokens per sequence
+MAX_ROW_ARRAYS = 8    # arrays of one hisa_cache_compact
+EMPTY_SLOT = -2       # parent of a slot that holds no drafted token
 
 
 class HisaParams(ctypes.Structure):
@@ -38,6 +44,12 @@ class HisaParams(ctypes.Structure):
         ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("d_head", ctypes.c_int32),
         ("scale", ctypes.c_float), ("flags", ctypes.c_int32), ("n_idx_heads", ctypes.c_int32),
     ]
+
+
+class HisaRows(ctypes.Structure):
+    """Mirror of hisa_rows_t."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
 
 
 class HisaError(RuntimeError):
@@ -83,6 +95,14 @@ def _load():
         "hisa_remap_ids": [vp, i64, ctypes.c_int32, i64, i64, i64, vp, vp],
         "hisa_lse_merge": [vp, vp, ctypes.c_int32, i64, ctypes.c_int32, vp, vp, vp],
         "hisa_sparse_attn_kernel": [pp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32)],
+        "hisa_tree_attn_workspace_size": [pp, ctypes.c_int32, sz],
+        "hisa_tree_attn_fwd": [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "hisa_cache_weight_workspace_size": [pp, sz],
+        "hisa_cache_weight": [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "hisa_cache_keep_workspace_size": [pp, sz],
+        "hisa_cache_keep": [pp, vp, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp,
+                            ctypes.c_size_t, vp],
+        "hisa_cache_compact": [pp, vp, ctypes.c_int32, vp, ctypes.POINTER(HisaRows), ctypes.c_int32, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -331,6 +351,149 @@ def hisa_lse_merge(o_parts, lse_parts, o, lse=None, stream=None):
                                                  _stream(stream)))
 
 
+# ---------------------------------------------------------------- a cache of bounded size, several drafted tokens
+
+def _refuse(call, detail):
+    raise HisaError(call, HISA_ERR_INVALID_ARG, detail)
+
+
+def _checked(call, device, **tensors):
+    """The addresses of name=(tensor, dtype, shape) in order.  The library takes dense tensors and trusts their
+    sizes, so each tensor has to be a contiguous CUDA tensor of that type and shape on `device` (None passes
+    through)."""
+    out = []
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            _refuse(call, f"{name}: expected a CUDA tensor, got one on {t.device}")
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            _refuse(call, f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_contiguous():
+            _refuse(call, f"{name}: expected a contiguous tensor, got strides {t.stride()}")
+        if t.device != device:
+            _refuse(call, f"{name}: expected a tensor on {device}, got one on {t.device}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _on_device(call, device, stream, fn):
+    """fn(stream) with `device` current, on `stream` or the current stream of that device."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        _refuse(call, f"the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = fn(stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(stream.cuda_stream)
+    _check(call, rc)
+
+
+def _status_and_workspace(call, device, dev_status, workspace, nbytes):
+    import torch
+
+    if workspace is None:
+        workspace = _workspace(nbytes, device)
+    st, ws = _checked(call, device, dev_status=(dev_status, torch.int32, (1,)),
+                      workspace=(workspace, torch.uint8, (workspace.numel(),)))
+    return st, ws, workspace
+
+
+def hisa_tree_attn_workspace_size(p, with_weight=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check("hisa_tree_attn_workspace_size",
+           _lib.hisa_tree_attn_workspace_size(ctypes.byref(p), 1 if with_weight else 0, ctypes.byref(n)))
+    return n.value
+
+
+def hisa_tree_attn_fwd(p, q, k, v, kv_len, o, lse=None, parent=None, weight=None, dev_status=None, workspace=None,
+                       stream=None):
+    """Attention of p.n_q drafted tokens per sequence over a cache of p.n_kv rows (see include/hisa.h): q, o
+    [b][n_q][H][d] and k, v [b][n_kv][Hk][d] bf16, kv_len [b] and parent [b][n_q] int32, lse [b][n_q][H] and
+    weight [b][n_kv] fp32."""
+    import torch
+
+    call, dev = "hisa_tree_attn_fwd", q.device
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    qs, ks = (p.batch, p.n_q, p.n_heads, p.d_head), (p.batch, p.n_kv, p.n_kv_heads, p.d_head)
+    a = _checked(call, dev, q=(q, bf, qs), k=(k, bf, ks), v=(v, bf, ks), kv_len=(kv_len, i32, (p.batch,)),
+                 parent=(parent, i32, (p.batch, p.n_q)), o=(o, bf, qs), lse=(lse, f32, qs[:3]),
+                 weight=(weight, f32, ks[:2]))
+    st, ws, workspace = _status_and_workspace(
+        call, dev, dev_status, workspace,
+        hisa_tree_attn_workspace_size(p, weight is not None) if workspace is None else 0)
+    _on_device(call, dev, stream,
+               lambda s: _lib.hisa_tree_attn_fwd(ctypes.byref(p), *a, st, ws, workspace.numel(), s))
+
+
+def hisa_cache_weight_workspace_size(p) -> int:
+    return _size(_lib.hisa_cache_weight_workspace_size, p)
+
+
+def hisa_cache_weight(p, q, k, kv_len, lse, weight, parent=None, path=None, dev_status=None, workspace=None,
+                      stream=None):
+    """The attention weight each cached row receives from the counted slots, into weight [b][n_kv] (see
+    include/hisa.h); path [b][n_q] int32: the accepted slots, ascending, -1 padded."""
+    import torch
+
+    call, dev = "hisa_cache_weight", q.device
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    qs, ks = (p.batch, p.n_q, p.n_heads, p.d_head), (p.batch, p.n_kv, p.n_kv_heads, p.d_head)
+    a = _checked(call, dev, q=(q, bf, qs), k=(k, bf, ks), kv_len=(kv_len, i32, (p.batch,)),
+                 parent=(parent, i32, (p.batch, p.n_q)), path=(path, i32, (p.batch, p.n_q)), lse=(lse, f32, qs[:3]),
+                 weight=(weight, f32, ks[:2]))
+    st, ws, workspace = _status_and_workspace(call, dev, dev_status, workspace,
+                                              hisa_cache_weight_workspace_size(p) if workspace is None else 0)
+    _on_device(call, dev, stream,
+               lambda s: _lib.hisa_cache_weight(ctypes.byref(p), *a, st, ws, workspace.numel(), s))
+
+
+def hisa_cache_keep_workspace_size(p) -> int:
+    return _size(_lib.hisa_cache_keep_workspace_size, p)
+
+
+def hisa_cache_keep(p, weight, kv_len, budget, keep_idx, kept_len, n_first=0, n_recent=0, dev_status=None,
+                    workspace=None, stream=None):
+    """The rows of each sequence to keep within `budget` (see include/hisa.h): keep_idx [b][budget] int32,
+    ascending, -1 padded, and kept_len [b] int32, from weight [b][n_kv] fp32."""
+    import torch
+
+    call, dev, i32 = "hisa_cache_keep", weight.device, torch.int32
+    w, n, ki, kl = _checked(call, dev, weight=(weight, torch.float32, (p.batch, p.n_kv)),
+                            kv_len=(kv_len, i32, (p.batch,)), keep_idx=(keep_idx, i32, (p.batch, budget)),
+                            kept_len=(kept_len, i32, (p.batch,)))
+    st, ws, workspace = _status_and_workspace(call, dev, dev_status, workspace,
+                                              hisa_cache_keep_workspace_size(p) if workspace is None else 0)
+    _on_device(call, dev, stream,
+               lambda s: _lib.hisa_cache_keep(ctypes.byref(p), w, n, budget, n_first, n_recent, ki, kl, st, ws,
+                                              workspace.numel(), s))
+
+
+def hisa_cache_compact(p, rows, arrays, dst_begin=None, dev_status=None, stream=None):
+    """Rows rows[s][j] of every array moved to dst_begin[s] + j, in place (see include/hisa.h).  arrays: tensors
+    [b][n_kv][...] of any types whose rows have a multiple of 4 bytes."""
+    import torch
+
+    call, dev, i32 = "hisa_cache_compact", rows.device, torch.int32
+    if rows.dim() != 2 or not 1 <= len(arrays) <= MAX_ROW_ARRAYS:
+        _refuse(call, f"expected rows [b][n] and 1 to {MAX_ROW_ARRAYS} arrays, got {tuple(rows.shape)} and "
+                      f"{len(arrays)}")
+    lead = (p.batch, p.n_kv)
+    r, d, st = _checked(call, dev, rows=(rows, i32, (p.batch, rows.shape[1])),
+                        dst_begin=(dst_begin, i32, (p.batch,)), dev_status=(dev_status, i32, (1,)))
+    c = (HisaRows * len(arrays))()
+    for i, t in enumerate(arrays):
+        c[i].base, = _checked(call, dev, **{f"arrays[{i}]": (t, t.dtype, lead + tuple(t.shape[2:]))})
+        c[i].row_bytes = math.prod(t.shape[2:]) * t.element_size()
+    _on_device(call, dev, stream,
+               lambda s: _lib.hisa_cache_compact(ctypes.byref(p), r, rows.shape[1], d, c, len(arrays), st, s))
+
+
 def hisa_gather_probe(rows, row_bytes, n_gathers, sink, seed=1, ctas_per_sm=0, stream=None):
     """Measurement helper: n_gathers copies of hashed rows of `rows` into shared memory, the
     attention kernel's gather pattern without its arithmetic (see include/hisa.h)."""
@@ -359,6 +522,28 @@ def forward(p, q_idx, k_idx, q, k, v, return_indices=False, stream=None, idx_wei
         tok = torch.empty((p.batch, p.n_q, p.top_k), dtype=torch.int32, device=dev)
     hisa_forward(p, q_idx, k_idx, q, k, v, o, lse, blk, tok, stream=stream, idx_weights=idx_weights)
     return (o, lse, blk, tok) if return_indices else (o, lse)
+
+
+def tree_attn(p, q, k, v, kv_len, parent=None, weight=None, stream=None):
+    """Allocate the outputs with torch and run hisa_tree_attn_fwd; returns (o, lse)."""
+    import torch
+
+    o = torch.empty((p.batch, p.n_q, p.n_heads, p.d_head), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((p.batch, p.n_q, p.n_heads), dtype=torch.float32, device=q.device)
+    hisa_tree_attn_fwd(p, q, k, v, kv_len, o, lse, parent=parent, weight=weight, stream=stream)
+    return o, lse
+
+
+def evict(p, weight, kv_len, budget, arrays, n_first=0, n_recent=0, stream=None):
+    """Shrink every sequence of the cache to at most `budget` rows: hisa_cache_keep on `weight` [b][n_kv], then
+    hisa_cache_compact of `arrays` ([b][n_kv][...] tensors) and of `weight`.  kv_len [b] int32 is updated in place;
+    returns the rows kept, keep_idx [b][budget].  Block keys of a moved cache have to be pooled again."""
+    import torch
+
+    keep = torch.empty((p.batch, budget), dtype=torch.int32, device=weight.device)
+    hisa_cache_keep(p, weight, kv_len, budget, keep, kv_len, n_first, n_recent, stream=stream)
+    hisa_cache_compact(p, keep, [*arrays, weight], stream=stream)
+    return keep
 
 
 def n_blocks(p) -> int:

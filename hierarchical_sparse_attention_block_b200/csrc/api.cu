@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -838,6 +839,110 @@ hisa_status_t hisa_gather_probe(const void* rows, int64_t n_rows, int32_t row_by
   if (n_gathers == 0) return HISA_OK;
   return hisa::cuda_fail(hisa::launch_gather_probe(rows, n_rows, row_bytes, n_gathers, seed, sink,
                                                      ctas_per_sm ? ctas_per_sm : 3, stream));
+}
+
+namespace {
+// Shape of a call on a cache of n_kv rows per sequence; drafts: n_q is the number of slots.
+hisa_status_t cache_shape(const hisa_params_t* p, bool drafts, Shape* s) {
+  const hisa_status_t rc = hisa::make_shape(p, false, drafts, s);
+  if (rc != HISA_OK) return rc;
+  if (drafts && (s->n_q > hisa::kMaxDraft || s->H > 1024)) return HISA_ERR_UNSUPPORTED;
+  return HISA_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ptrs) {  // null pointers count as aligned
+  for (const void* p : ptrs)
+    if (!hisa::aligned16(p)) return false;
+  return true;
+}
+}  // namespace
+
+hisa_status_t hisa_tree_attn_workspace_size(const hisa_params_t* params, int32_t with_weight, size_t* bytes) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, true, &s);
+  if (rc != HISA_OK) return rc;
+  if (!bytes || with_weight < 0 || with_weight > 1) return HISA_ERR_INVALID_ARG;
+  *bytes = hisa::tree_attn_workspace_bytes(s, with_weight != 0);
+  return HISA_OK;
+}
+
+hisa_status_t hisa_tree_attn_fwd(const hisa_params_t* params, const void* q, const void* k, const void* v,
+                                 const int32_t* kv_len, const int32_t* parent, void* o, float* lse, float* weight,
+                                 int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, true, &s);
+  if (rc != HISA_OK) return rc;
+  if (!q || !k || !v || !kv_len || !o) return HISA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, kv_len, parent, o, lse, weight})) return HISA_ERR_INVALID_ARG;
+  const size_t need = hisa::tree_attn_workspace_bytes(s, weight != nullptr);
+  if (need > 0 && (!workspace || workspace_bytes < need || !hisa::aligned16(workspace))) return HISA_ERR_WORKSPACE;
+  return hisa::cuda_fail(
+      hisa::launch_tree_attn(s, q, k, v, kv_len, parent, o, lse, weight, dev_status, workspace, stream));
+}
+
+hisa_status_t hisa_cache_weight_workspace_size(const hisa_params_t* params, size_t* bytes) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, true, &s);
+  if (rc != HISA_OK) return rc;
+  if (!bytes) return HISA_ERR_INVALID_ARG;
+  *bytes = hisa::cache_weight_workspace_bytes(s);
+  return HISA_OK;
+}
+
+hisa_status_t hisa_cache_weight(const hisa_params_t* params, const void* q, const void* k, const int32_t* kv_len,
+                                const int32_t* parent, const int32_t* path, const float* lse, float* weight,
+                                int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, true, &s);
+  if (rc != HISA_OK) return rc;
+  if (!q || !k || !kv_len || !lse || !weight) return HISA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, kv_len, parent, path, lse, weight})) return HISA_ERR_INVALID_ARG;
+  const size_t need = hisa::cache_weight_workspace_bytes(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || !hisa::aligned16(workspace))) return HISA_ERR_WORKSPACE;
+  return hisa::cuda_fail(
+      hisa::launch_cache_weight(s, q, k, kv_len, parent, path, lse, weight, dev_status, workspace, stream));
+}
+
+hisa_status_t hisa_cache_keep_workspace_size(const hisa_params_t* params, size_t* bytes) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, false, &s);
+  if (rc != HISA_OK) return rc;
+  if (!bytes) return HISA_ERR_INVALID_ARG;
+  *bytes = hisa::cache_keep_workspace_bytes(s);
+  return HISA_OK;
+}
+
+hisa_status_t hisa_cache_keep(const hisa_params_t* params, const float* weight, const int32_t* kv_len, int32_t budget,
+                              int32_t n_first, int32_t n_recent, int32_t* keep_idx, int32_t* kept_len,
+                              int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, false, &s);
+  if (rc != HISA_OK) return rc;
+  if (!weight || !kv_len || !keep_idx || !kept_len) return HISA_ERR_INVALID_ARG;
+  if (!all_aligned16({weight, kv_len, keep_idx, kept_len})) return HISA_ERR_INVALID_ARG;
+  if (budget < 1 || budget > s.n_kv || n_first < 0 || n_recent < 0 || (int64_t)n_first + n_recent > budget)
+    return HISA_ERR_INVALID_ARG;
+  const size_t need = hisa::cache_keep_workspace_bytes(s);
+  if (need > 0 && (!workspace || workspace_bytes < need || !hisa::aligned16(workspace))) return HISA_ERR_WORKSPACE;
+  return hisa::cuda_fail(hisa::launch_cache_keep(s, weight, kv_len, budget, n_first, n_recent, keep_idx, kept_len,
+                                                 dev_status, workspace, stream));
+}
+
+hisa_status_t hisa_cache_compact(const hisa_params_t* params, const int32_t* rows, int32_t n_rows,
+                                 const int32_t* dst_begin, const hisa_rows_t* arrays, int32_t n_arrays,
+                                 int32_t* dev_status, cudaStream_t stream) {
+  Shape s;
+  const hisa_status_t rc = cache_shape(params, false, &s);
+  if (rc != HISA_OK) return rc;
+  if (!rows || !arrays || !all_aligned16({rows, dst_begin})) return HISA_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_rows > s.n_kv || n_arrays < 1 || n_arrays > hisa::kMaxRowArrays) return HISA_ERR_INVALID_ARG;
+  for (int a = 0; a < n_arrays; ++a) {
+    if (!arrays[a].base || !hisa::aligned16(arrays[a].base)) return HISA_ERR_INVALID_ARG;
+    if (arrays[a].row_bytes < 4 || arrays[a].row_bytes > (1 << 24) || arrays[a].row_bytes % 4 != 0)
+      return HISA_ERR_INVALID_ARG;
+  }
+  return hisa::cuda_fail(
+      hisa::launch_cache_compact(s, rows, n_rows, dst_begin, arrays, n_arrays, dev_status, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,184 @@
+// hisa_cache_compact: rows of the cache moved towards the front, in place.
+//
+//   array[s][begin + j] = array[s][rows[s][j]],  rows ascending, rows[s][j] >= begin + j.
+//
+// In place, a destination row may be the source of another entry.  Every source is at or behind its
+// own destination and the sources ascend, so a sweep over j in ascending order that has read the
+// rows of entries [0, j1) may write the destinations [0, j1): a later entry's source lies at
+// begin + j1 or behind.  One CTA therefore owns a slice of at most 128 bytes of every row of one
+// sequence and sweeps the list in tiles: it loads the next tile's rows into registers, passes a
+// barrier (every load of the current tile is then in), and writes the current tile.  CTAs share no
+// byte, so nothing else has to be ordered.  The bound is HBM: each moved byte is read and written
+// once; the next tile's loads are in flight while the current one is stored.
+#include "common.cuh"
+#include "internal.h"
+
+namespace hisa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 8;    // row loads in flight per thread and tile
+constexpr int kLanesMax = 8;  // threads per row slice
+
+struct Array {
+  uint8_t* base;
+  int64_t row_bytes;
+  int first_slice;  // first slice id of this array
+  int vec;          // bytes per access: 16, or 4 where the rows are no multiple of 16
+  int lanes;        // threads per row slice: a power of two up to kLanesMax
+};
+struct Arrays {
+  Array a[kMaxRowArrays];
+  int n;
+};
+
+// Plain loads (never the read-only path: the kernel writes the same array).
+template <class V>
+__device__ __forceinline__ V load_once(const uint8_t* p) {
+  return *reinterpret_cast<const V*>(p);
+}
+
+// The entries of one tile, checked: src[j] = the source row, or -1 for an entry that moves nothing.
+struct Tile {
+  int32_t src[kThreads * kUnroll];
+};
+
+template <class V>
+__device__ __forceinline__ void sweep(const Array& A, int slice, const int32_t* __restrict__ list, int n, int64_t begin,
+                                      int64_t n_kv, int64_t seq, Tile (&tile)[2], int32_t* status) {
+  const int tid = threadIdx.x;
+  const int per = kThreads / A.lanes;  // rows per step
+  const int rows = per * kUnroll;      // entries per tile
+  const int r0 = tid / A.lanes, c = tid & (A.lanes - 1);
+  const int64_t col = ((int64_t)slice * A.lanes + c) * (int64_t)sizeof(V);
+  const bool mine = col < A.row_bytes;
+  uint8_t* base = A.base + seq * n_kv * A.row_bytes + col;
+  __shared__ int32_t last_in;  // largest in-range entry of the tiles checked so far
+  __shared__ int dirty;        // a tile broke the order: later tiles are checked entry by entry
+  if (tid == 0) {
+    last_in = -1;
+    dirty = 0;
+  }
+  __syncthreads();
+
+  // Reads and checks the entries [j0, j0 + rows) into t.  An ascending list with its padding at the
+  // end passes the test of neighbours; any other tile, and every tile after it, is checked by one
+  // thread in order.  All threads call; ends synchronised.
+  auto check = [&](int64_t j0, Tile& t) {
+    bool clean = true;
+    for (int i = tid; i < rows; i += kThreads) {
+      const int64_t j = j0 + i;
+      int32_t r = -1;
+      if (j < n) {
+        r = list[j];
+        const int32_t before = j > 0 ? list[j - 1] : -1;
+        const bool in = r >= begin + j && r < n_kv;
+        clean = clean && (r == -1 || (in && r > before && (j == 0 || before >= 0)));
+      }
+      t.src[i] = r;
+    }
+    if (!__syncthreads_and(clean && !dirty)) {
+      if (tid == 0) {
+        int32_t last = last_in;
+        bool bad = false;
+        if (!dirty) {  // every tile before was clean: its last entry that is no padding is the largest
+          int64_t j = j0 - 1;
+          while (j >= 0 && list[j] == -1) --j;
+          if (j >= 0) last = list[j];
+        }
+        for (int i = 0; i < rows && j0 + i < n; ++i) {
+          const int32_t r = t.src[i];
+          if (r == -1) continue;
+          if (!(r >= begin + j0 + i && r < n_kv)) {
+            t.src[i] = -1;
+            bad = true;
+          } else if (r <= last) {
+            t.src[i] = -1;
+            bad = true;
+          } else {
+            last = r;
+          }
+        }
+        last_in = last;
+        dirty = 1;
+        if (bad && status) atomicOr(status, kStatusBadIndex);
+      }
+      __syncthreads();
+    }
+  };
+
+  V cur[kUnroll], nxt[kUnroll];
+  auto load = [&](const Tile& t, V (&x)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int32_t r = t.src[u * per + r0];
+      if (mine && r >= 0) x[u] = load_once<V>(base + (int64_t)r * A.row_bytes);
+    }
+  };
+  check(0, tile[0]);
+  load(tile[0], cur);
+  int b = 0;
+  for (int64_t j0 = 0; j0 < n; j0 += rows, b ^= 1) {
+    const bool more = j0 + rows < n;
+    if (more) {
+      check(j0 + rows, tile[b ^ 1]);
+      load(tile[b ^ 1], nxt);
+    }
+    __syncthreads();  // the rows of the current tile are read by every thread
+    const Tile& t = tile[b];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int e = u * per + r0;
+      const int32_t r = t.src[e];
+      if (mine && r >= 0 && r != begin + j0 + e) *reinterpret_cast<V*>(base + (begin + j0 + e) * A.row_bytes) = cur[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
+    __syncthreads();  // tile[b] may be filled again
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+    cache_compact_kernel(const __grid_constant__ Arrays arrays, const int32_t* __restrict__ rows, int n_rows,
+                         const int32_t* __restrict__ dst_begin, int64_t n_kv, int32_t* __restrict__ status) {
+  __shared__ Tile tile[2];
+  const int64_t seq = blockIdx.y;
+  int a = 0;
+  while (a + 1 < arrays.n && (int)blockIdx.x >= arrays.a[a + 1].first_slice) ++a;
+  const Array& A = arrays.a[a];
+  const int slice = (int)blockIdx.x - A.first_slice;
+  const int64_t begin = dst_begin ? dst_begin[seq] : 0;
+  if (begin < 0) {
+    if (threadIdx.x == 0 && status) atomicOr(status, kStatusBadIndex);
+    return;
+  }
+  if (A.vec == 16)
+    sweep<uint4>(A, slice, rows + seq * n_rows, n_rows, begin, n_kv, seq, tile, status);
+  else
+    sweep<uint32_t>(A, slice, rows + seq * n_rows, n_rows, begin, n_kv, seq, tile, status);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_compact(const Shape& s, const int32_t* rows, int n_rows, const int32_t* dst_begin,
+                                 const hisa_rows_t* arrays, int n_arrays, int32_t* status, cudaStream_t st) {
+  Arrays p;
+  p.n = n_arrays;
+  int64_t slices = 0;
+  for (int i = 0; i < n_arrays; ++i) {
+    Array& A = p.a[i];
+    A.base = static_cast<uint8_t*>(arrays[i].base);
+    A.row_bytes = arrays[i].row_bytes;
+    A.vec = A.row_bytes % 16 == 0 ? 16 : 4;
+    const int64_t units = A.row_bytes / A.vec;
+    A.lanes = 1;
+    while (A.lanes < kLanesMax && A.lanes < units) A.lanes *= 2;
+    A.first_slice = (int)slices;
+    slices += (units + A.lanes - 1) / A.lanes;
+  }
+  cache_compact_kernel<<<dim3((unsigned)slices, (unsigned)s.batch), kThreads, 0, st>>>(p, rows, n_rows, dst_begin,
+                                                                                       s.n_kv, status);
+  return cudaGetLastError();
+}
+
+}  // namespace hisa

@@ -103,6 +103,24 @@ cudaError_t launch_remap_ids(const int32_t* in, int64_t rows, int cols, int64_t 
 cudaError_t launch_lse_merge(const void* o_parts, const float* lse_parts, int G, int64_t rows, int d, void* o,
                              float* lse, cudaStream_t st);
 
+// Drafted tokens over a cache of bounded size (see the hisa_tree_attn_fwd family in hisa.h).
+constexpr int kMaxDraft = 256;  // slots per sequence
+size_t tree_attn_workspace_bytes(const Shape& s, bool with_weight);
+cudaError_t launch_tree_attn(const Shape& s, const void* q, const void* k, const void* v, const int32_t* kv_len,
+                             const int32_t* parent, void* o, float* lse, float* weight, int32_t* status, void* ws,
+                             cudaStream_t st);
+size_t cache_weight_workspace_bytes(const Shape& s);
+cudaError_t launch_cache_weight(const Shape& s, const void* q, const void* k, const int32_t* kv_len,
+                                const int32_t* parent, const int32_t* path, const float* lse, float* weight,
+                                int32_t* status, void* ws, cudaStream_t st);
+size_t cache_keep_workspace_bytes(const Shape& s);
+cudaError_t launch_cache_keep(const Shape& s, const float* weight, const int32_t* kv_len, int budget, int n_first,
+                              int n_recent, int32_t* keep_idx, int32_t* kept_len, int32_t* status, void* ws,
+                              cudaStream_t st);
+constexpr int kMaxRowArrays = 8;
+cudaError_t launch_cache_compact(const Shape& s, const int32_t* rows, int n_rows, const int32_t* dst_begin,
+                                 const hisa_rows_t* arrays, int n_arrays, int32_t* status, cudaStream_t st);
+
 // Measurement helper: gathers of hashed rows into shared memory (see hisa_gather_probe).
 bool gather_probe_row_bytes_ok(int row_bytes);
 cudaError_t launch_gather_probe(const void* rows, int64_t n_rows, int row_bytes, int64_t n_gathers, uint32_t seed,

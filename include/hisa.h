@@ -317,6 +317,100 @@ hisa_status_t hisa_remap_ids(const int32_t* in, int64_t rows, int32_t cols, int6
 hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_t n_parts, int64_t rows, int32_t d,
                              void* o, float* lse, cudaStream_t stream);
 
+/* ---- A KV cache of bounded size, several drafted tokens a step ----
+ * Calls of a decode loop that keeps its cache small and verifies several
+ * drafted tokens at once; the attention here is dense over the rows the cache
+ * holds.  The pages keep the whole cache ([QB] "HISA的關鍵優勢在於": the KV cache
+ * is unchanged), so these steps have no counterpart there; they share the
+ * tensors of the calls above.  `params` gives batch, n_q (T, the slots for
+ * drafted tokens, 1..256; HISA_ERR_UNSUPPORTED above), n_kv (the ROWS the
+ * cache has per sequence), n_heads, n_kv_heads, d_head and scale.
+ *   kv_len [b] int32, device: context rows of each sequence; rows [0, L) of
+ *     sequence s are its context (L = kv_len[s]) and row L + i holds the key
+ *     and value of drafted token i.  0 <= L and L + T <= n_kv; a sequence that
+ *     breaks this is skipped (its outputs as for empty slots, nothing
+ *     accumulated) and sets bit 0 of *dev_status.  What other rows hold is
+ *     never used (NaN and infinities included).
+ *   parent [b][T] int32, device: the tree.  parent[s][i] = j < i: token i
+ *     follows drafted token j; -1: it follows the context; -2: the slot is
+ *     empty.  Any other value makes the slot empty and sets bit 0 of
+ *     *dev_status; a slot that follows an empty one is empty.  NULL: a chain
+ *     (token i follows i - 1; T = 1 is a plain decode step).
+ *   Token i sees the context, its ancestors and itself:
+ *     V(i) = [0, L) and L + j for j in anc(i) or j = i.
+ * A step: append the drafted tokens' rows -> hisa_tree_attn_fwd -> (accept a
+ * path) -> hisa_cache_weight for the accepted tokens -> hisa_cache_compact
+ * moves their rows to the context's end; once the cache is full,
+ * hisa_cache_keep and hisa_cache_compact shrink it to its budget. */
+
+/* Attention of drafted tokens over the cache: for every slot i and head h (kv
+ * head g = h / (H / Hk)), with z(t) = scale * q[s][i][h] . k[s][t][g],
+ *   o[s][i][h]   = sum_{t in V(i)} softmax_t(z(t)) v[s][t][g]
+ *   lse[s][i][h] = ln sum_{t in V(i)} exp(z(t))       (lse nullable)
+ * An empty slot gives o = 0, lse = -inf.
+ * weight (nullable) [b][n_kv] fp32: the attention weight each row receives,
+ *   a(t) = sum over slots i with t in V(i) and heads h of exp(z(t) - lse[s][i][h]),
+ * is added on the context's rows (weight[s][t] += a(t), t < L) and replaces
+ * what the drafted rows held (weight[s][t] = a(t), L <= t < L + T; 0 for an
+ * empty slot's row); later rows stay as they are.  Where drafted tokens may be
+ * rejected, pass NULL and call hisa_cache_weight for the accepted ones.
+ * Workspace: hisa_tree_attn_workspace_size bytes (with_weight: 1 if weight is
+ * passed, 0 if not), 16-byte aligned, used by one call at a time. */
+hisa_status_t hisa_tree_attn_workspace_size(const hisa_params_t* params, int32_t with_weight, size_t* bytes);
+hisa_status_t hisa_tree_attn_fwd(const hisa_params_t* params, const void* q, const void* k, const void* v,
+                                 const int32_t* kv_len, const int32_t* parent, void* o, float* lse, float* weight,
+                                 int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The attention weight alone, from queries and the LSE their attention gave:
+ * a(t) and its place in `weight` as above, summed over the counted slots.
+ * path (nullable) [b][T] int32: the counted slots of each sequence, ascending,
+ * -1 padded (entries out of range or out of order are skipped and set bit 0 of
+ * *dev_status); NULL counts every slot.  A row of lse that is -inf counts
+ * nothing.  Only K is read, once for all counted slots.  A prompt's last
+ * tokens are a chain of T slots behind the first n - T rows.  The sums are
+ * formed in a fixed order: equal inputs give equal bits. */
+hisa_status_t hisa_cache_weight_workspace_size(const hisa_params_t* params, size_t* bytes);
+hisa_status_t hisa_cache_weight(const hisa_params_t* params, const void* q, const void* k, const int32_t* kv_len,
+                                const int32_t* parent, const int32_t* path, const float* lse, float* weight,
+                                int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The rows of each sequence to keep within a budget: all L = kv_len[s] of them
+ * when L <= budget, else the first n_first, the last n_recent and, of the rows
+ * between, the budget - n_first - n_recent with the largest weight (ties: lower
+ * row first; -0 equals +0, every NaN ranks above +inf, all of them alike).
+ * keep_idx [b][budget] int32: ascending, -1 padded; kept_len [b] int32:
+ * min(L, budget) (may be kv_len itself).  0 <= L <= n_kv, else the list
+ * is all -1, kept_len 0 and bit 0 of *dev_status is set.  budget in [1, n_kv],
+ * n_first, n_recent >= 0, n_first + n_recent <= budget.  Uses batch and n_kv of
+ * params. */
+hisa_status_t hisa_cache_keep_workspace_size(const hisa_params_t* params, size_t* bytes);
+hisa_status_t hisa_cache_keep(const hisa_params_t* params, const float* weight, const int32_t* kv_len, int32_t budget,
+                              int32_t n_first, int32_t n_recent, int32_t* keep_idx, int32_t* kept_len,
+                              int32_t* dev_status, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One per-row array of the cache: [b][n_kv] rows of row_bytes bytes each (a
+ * multiple of 4, at most 2^24), device memory, 16-byte aligned. */
+typedef struct hisa_rows {
+  void* base;
+  int64_t row_bytes;
+} hisa_rows_t;
+
+/* Moves rows towards the front, in place, in every given array (K, V, the
+ * indexer keys, weights, positions):
+ *   array[s][dst_begin[s] + j] = array[s][rows[s][j]]   for j = 0 .. n_rows - 1,
+ * all rows read as they were before the call.  rows [b][n_rows] int32:
+ * ascending, -1 padded.  dst_begin (nullable: 0) [b] int32.  After
+ * hisa_cache_keep, rows = keep_idx; to commit the accepted tokens of a tree,
+ * rows = kv_len + path and dst_begin = kv_len.  An entry below dst_begin[s] + j,
+ * at or above n_kv or not greater than every in-range entry before it is
+ * skipped, with bit 0 of *dev_status; its destination row stays as it is, as
+ * does every row that is no destination.  A negative dst_begin[s] skips the
+ * sequence the same way.  arrays: host array of 1..8 entries that do not
+ * overlap.  Uses batch and n_kv of params. */
+hisa_status_t hisa_cache_compact(const hisa_params_t* params, const int32_t* rows, int32_t n_rows,
+                                 const int32_t* dst_begin, const hisa_rows_t* arrays, int32_t n_arrays,
+                                 int32_t* dev_status, cudaStream_t stream);
+
 /* Measurement helper, not a step of the method (the pages have no
  * counterpart): n_gathers copies of row h(e) (row_bytes each; h a hash of the
  * gather number e and seed, uniform over [0, n_rows)) into shared memory with
