@@ -33,7 +33,7 @@ __device__ bool draft_tree_build(DraftTree& t, const int32_t* parent, int T, int
   bool bad = false;
   for (int i = tid; i < T; i += NT) {
     if (parent == nullptr) {
-      for (int w = 0; w < nw; ++w) {
+      for (int w = 0; w < kDraftWords; ++w) {
         const int hi = i - 32 * w;  // bits 0 .. hi of word w
         t.anc[i][w] = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
       }
@@ -43,7 +43,7 @@ __device__ bool draft_tree_build(DraftTree& t, const int32_t* parent, int T, int
     const int p = parent[i];
     const bool ok = p >= -1 && p < i;
     bad = bad || (!ok && p != -2);
-    for (int w = 0; w < nw; ++w) t.anc[i][w] = w == (i >> 5) ? 1u << (i & 31) : 0u;
+    for (int w = 0; w < kDraftWords; ++w) t.anc[i][w] = w == (i >> 5) ? 1u << (i & 31) : 0u;
     t.up[i] = (int16_t)(ok ? p : kEmpty);
   }
   sync();
