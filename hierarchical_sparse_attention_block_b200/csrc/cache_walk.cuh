@@ -1,0 +1,152 @@
+// How the kernels over a cache share their work: every key tile of every item (a part of one
+// sequence's work that reads all its key tiles) is a unit, the units lie in the order sequence, item,
+// key tile, and CTA c takes the c-th of equal contiguous ranges.  The ranges follow from the lengths
+// on the device, so ragged caches balance and one long cache covers every SM.
+#pragma once
+
+#include "common.cuh"
+#include "draft_tree.cuh"
+
+namespace hisa {
+
+constexpr int kTileKeys = 128;  // cache rows per key tile
+constexpr int kMaxCtas = 148;   // one CTA per SM
+
+__device__ __forceinline__ int64_t key_tiles(int64_t L, int T) {
+  return L < 0 ? 0 : (L + T + kTileKeys - 1) / kTileKeys;
+}
+
+// CTA c of `ctas` takes the units [range_begin(c), range_begin(c + 1)), at least one each: with fewer
+// units than CTAs the CTAs behind the last unit take none.
+__device__ __forceinline__ int64_t range_ctas(int64_t units, int64_t grid) { return units < grid ? units : grid; }
+__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t units, int64_t ctas) { return c * units / ctas; }
+// The CTA whose range holds unit u.
+__device__ __forceinline__ int64_t range_of(int64_t u, int64_t units, int64_t ctas) {
+  return ((u + 1) * ctas - 1) / units;
+}
+
+// One CTA's walk through its range, in segments: consecutive key tiles of one item.
+struct Walk {
+  const int32_t* kv_len;
+  int64_t n_kv, u, u1, first;  // first: the range's begin
+  int64_t P;                   // key tiles of the sequences before s
+  int64_t L, tiles;
+  int s, T, per_seq;           // per_seq: items of a sequence
+  // the segment: key tiles [j0, j0 + n) of the item
+  int item, j0, n;
+  int64_t start;
+
+  __device__ void at(int seq) {
+    s = seq;
+    L = context_len(kv_len, seq, T, n_kv);
+    tiles = key_tiles(L, T);
+  }
+  __device__ bool next() {
+    if (u >= u1) return false;
+    while (u >= (P + tiles) * per_seq) {
+      P += tiles;
+      at(s + 1);
+    }
+    const int64_t rel = u - P * per_seq;
+    item = (int)(rel / tiles);
+    j0 = (int)(rel - (int64_t)item * tiles);
+    n = (int)min(tiles - j0, u1 - u);
+    start = u;
+    u += n;
+    return true;
+  }
+  __device__ bool whole() const { return j0 == 0 && n == tiles; }
+  // Which of the CTA's segments that are not whole this one is: the range's first, or its last.
+  __device__ int slot() const { return start == first ? 0 : 1; }
+};
+
+template <int NT>
+struct WalkShared {
+  int64_t sums[NT / 32], found[2];
+};
+
+// The CTA's walk; all NT threads call, two barriers.  prefix (nullable, [batch + 1]): CTA 0 writes the
+// key tiles of the sequences before each, and of all; it also flags lengths out of range.
+template <int NT>
+__device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch, int per_seq, WalkShared<NT>& sm,
+                           int64_t* prefix, int32_t* status) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // every thread counts the key tiles of a run of sequences
+  const int run = (batch + NT - 1) / NT;
+  const int s0 = min(tid * run, batch), s1 = min(s0 + run, batch);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int s = s0; s < s1; ++s) {
+    const int64_t L = context_len(kv_len, s, T, n_kv);
+    bad = bad || L < 0;
+    mine += key_tiles(L, T);
+  }
+  if (bad && status && blockIdx.x == 0) atomicOr(status, kStatusBadIndex);
+  int64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sm.sums[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t x = sm.sums[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  const int64_t units = total * per_seq, ctas = range_ctas(units, gridDim.x);
+  const bool busy = blockIdx.x < ctas;
+  Walk walk;
+  walk.kv_len = kv_len;
+  walk.n_kv = n_kv;
+  walk.T = T;
+  walk.per_seq = per_seq;
+  walk.u = walk.first = busy ? range_begin(blockIdx.x, units, ctas) : 0;
+  walk.u1 = busy ? range_begin(blockIdx.x + 1, units, ctas) : 0;
+  if (busy && walk.u >= before * per_seq && walk.u < (before + mine) * per_seq) {
+    int64_t P = before;
+    for (int s = s0; s < s1; ++s) {
+      const int64_t n = key_tiles(context_len(kv_len, s, T, n_kv), T);
+      if (walk.u < (P + n) * per_seq) {
+        sm.found[0] = s;
+        sm.found[1] = P;
+        break;
+      }
+      P += n;
+    }
+  }
+  if (prefix && blockIdx.x == 0) {
+    int64_t P = before;
+    for (int s = s0; s < s1; ++s) {
+      prefix[s] = P;
+      P += key_tiles(context_len(kv_len, s, T, n_kv), T);
+    }
+    if (tid == 0) prefix[batch] = total;
+  }
+  __syncthreads();
+  if (busy) {
+    walk.P = sm.found[1];
+    walk.at((int)sm.found[0]);
+  }
+  return walk;
+}
+
+// 32 bits of a tail tile's mask: keys off .. off + 31 relative to the context's end.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* anc, int off) {
+  if (off <= -32) return 0xFFFFFFFFu;
+  if (off >= kMaxDraft) return 0u;
+  if (off < 0) return (anc[0] << -off) | ((1u << -off) - 1u);
+  const int w = off >> 5, sh = off & 31;
+  const uint32_t lo = anc[w], hi = w + 1 < kDraftWords ? anc[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+// The same for a chain: slot i sees the keys off <= i.
+__device__ __forceinline__ uint32_t chain_word(int i, int off) {
+  const int n = i - off + 1;  // visible keys of the word
+  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
+}  // namespace hisa

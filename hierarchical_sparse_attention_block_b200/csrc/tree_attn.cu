@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include "attn_math.cuh"
+#include "cache_walk.cuh"
 #include "common.cuh"
 #include "draft_tree.cuh"
 #include "internal.h"
@@ -41,8 +42,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 128;     // query rows per tile = keys per key tile
-constexpr int kMaxCtas = 148;  // one per SM
+constexpr int kRows = kTileKeys;  // query rows per tile = keys per key tile
 constexpr uint32_t kTmemCols = 512;
 constexpr int kHalf = kRows * 128;  // 64 columns of 128 rows of 16-bit values: one 128-byte swizzle span
 constexpr float kLn2 = 0.69314718055994531f;
@@ -71,8 +71,9 @@ struct Cfg {
     B_DRAIN,
     kNBar
   };
-  static constexpr int MISC_OFF = BAR_OFF + kNBar * 8;
-  static constexpr int kSmem = MISC_OFF + (int)sizeof(int64_t) * (kThreads + 8) + 128 + 1024;
+  static constexpr int WALK_OFF = BAR_OFF + kNBar * 8;
+  static constexpr int MISC_OFF = WALK_OFF + (int)sizeof(WalkShared<kThreads>);
+  static constexpr int kSmem = MISC_OFF + 4 * (2 + 2 * kDraftWords) + 1024;  // + slack for the 1024-byte alignment
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * (uint32_t)t; }
 };
@@ -83,66 +84,6 @@ struct Work {
   float* part_o;    // [cta][2][NT * 128][D]
   float2* part_ml;  // [cta][2][NT * 128]: max (log2 domain), sum
 };
-
-// CTA c of `ctas` takes the units [range_begin(c), range_begin(c + 1)), at least one each: with fewer
-// units than CTAs the CTAs behind the last unit take none.
-__device__ __forceinline__ int64_t range_ctas(int64_t units, int64_t grid) { return units < grid ? units : grid; }
-__device__ __forceinline__ int64_t range_begin(int64_t c, int64_t total, int64_t ctas) { return c * total / ctas; }
-// The CTA whose range holds unit u.
-__device__ __forceinline__ int64_t range_of(int64_t u, int64_t total, int64_t ctas) { return ((u + 1) * ctas - 1) / total; }
-
-__device__ __forceinline__ int64_t key_tiles(int64_t L, int T) { return L < 0 ? 0 : (L + T + kRows - 1) / kRows; }
-
-// One CTA's walk through its range: segments of consecutive key tiles of one item.
-struct Walk {
-  const int32_t* kv_len;
-  int64_t n_kv, u, u1, first;  // first: the range's begin
-  int64_t P;                   // key tiles of the sequences before s
-  int64_t L, tiles;
-  int s, T, per_seq, np;       // per_seq: items of a sequence
-  // the segment
-  int g, pair, j0, n;
-  int64_t start;
-
-  __device__ void at(int seq) {
-    s = seq;
-    L = context_len(kv_len, seq, T, n_kv);
-    tiles = key_tiles(L, T);
-  }
-  __device__ bool next() {
-    if (u >= u1) return false;
-    while (u >= (P + tiles) * per_seq) {
-      P += tiles;
-      at(s + 1);
-    }
-    const int64_t rel = u - P * per_seq;
-    const int item = (int)(rel / tiles);
-    g = item / np;
-    pair = item - g * np;
-    j0 = (int)(rel - (int64_t)item * tiles);
-    n = (int)min(tiles - j0, u1 - u);
-    start = u;
-    u += n;
-    return true;
-  }
-  __device__ bool whole() const { return j0 == 0 && n == tiles; }
-  __device__ int slot() const { return start == first ? 0 : 1; }  // of a segment that is not whole
-};
-
-// 32 bits of a tail tile's mask: keys off .. off + 31 relative to the context's end.
-__device__ __forceinline__ uint32_t mask_word(const uint32_t* anc, int off) {
-  if (off <= -32) return 0xFFFFFFFFu;
-  if (off >= kMaxDraft) return 0u;
-  if (off < 0) return (anc[0] << -off) | ((1u << -off) - 1u);
-  const int w = off >> 5, sh = off & 31;
-  const uint32_t lo = anc[w], hi = w + 1 < kDraftWords ? anc[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, sh);
-}
-// The same for a chain: slot i sees the keys off <= i.
-__device__ __forceinline__ uint32_t chain_word(int i, int off) {
-  const int n = i - off + 1;  // visible keys of the word
-  return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
@@ -157,9 +98,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) { return sb + (uint32_t)C::BAR_OFF + 8u * (uint32_t)i; };
   DraftTree& tree = *reinterpret_cast<DraftTree*>(smem + C::TREE_OFF);
-  int64_t* sums = reinterpret_cast<int64_t*>(smem + (C::MISC_OFF + 7) / 8 * 8);  // [kThreads]
-  int64_t* found = sums + C::kThreads;                                           // total, sequence, its prefix
-  uint32_t* misc = reinterpret_cast<uint32_t*>(found + 4);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   uint32_t* odd_rows = misc + 2;  // [2][kDraftWords]: drafted V rows with values that are not finite, per segment parity
@@ -183,71 +122,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     mbar_init_fence();
   }
   if (tid < 2 * kDraftWords) odd_rows[tid] = 0u;
-  // The units of the call: every thread counts the key tiles of a run of sequences.
-  const int R = T * (H / Hkv), np = (R + NT * kRows - 1) / (NT * kRows), per_seq = Hkv * np;
-  const int run = (batch + C::kThreads - 1) / C::kThreads;
-  const int s0 = min(tid * run, batch), s1 = min(s0 + run, batch);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += key_tiles(context_len(kv_len, s, T, n_kv), T);
-  {
-    int64_t incl = mine;  // inclusive prefix within the warp, then over the warps' sums
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-      if (lane >= off) incl += x;
-    }
-    sums[tid] = incl;
-  }
+  const int G = H / Hkv, R = T * G, np = (R + NT * kRows - 1) / (NT * kRows);  // items: (KV head, row-tile pair)
   tc_fence_before();
-  __syncthreads();
+  Walk walk = walk_begin<C::kThreads>(kv_len, n_kv, T, batch, Hkv * np,
+                                      *reinterpret_cast<WalkShared<C::kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int64_t before = sums[tid] - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    const int64_t x = sums[w * 32 + 31];
-    if (w < warp) before += x;
-    total += x;
-  }
-  const int64_t units = total * per_seq;
-  const int64_t ctas = range_ctas(units, gridDim.x);
-  const bool busy = blockIdx.x < ctas;
-  const int64_t u0 = busy ? range_begin(blockIdx.x, units, ctas) : 0;
-  const int64_t u1 = busy ? range_begin(blockIdx.x + 1, units, ctas) : 0;
-  if (busy && u0 >= before * per_seq && u0 < (before + mine) * per_seq) {
-    int64_t P = before;
-    for (int s = s0; s < s1; ++s) {
-      const int64_t n = key_tiles(context_len(kv_len, s, T, n_kv), T);
-      if (u0 < (P + n) * per_seq) {
-        found[0] = s;
-        found[1] = P;
-        break;
-      }
-      P += n;
-    }
-  }
-  if (blockIdx.x == 0) {
-    int64_t P = before;
-    for (int s = s0; s < s1; ++s) {
-      work.prefix[s] = P;
-      P += key_tiles(context_len(kv_len, s, T, n_kv), T);
-    }
-    if (tid == 0) work.prefix[batch] = total;
-  }
-  __syncthreads();
-  Walk walk;
-  walk.kv_len = kv_len;
-  walk.n_kv = n_kv;
-  walk.u = walk.first = u0;
-  walk.u1 = u1;
-  walk.T = T;
-  walk.per_seq = per_seq;
-  walk.np = np;
-  if (busy) {
-    walk.P = found[1];
-    walk.at((int)found[0]);
-  }
-  const int G = H / Hkv;
 
   if (warp == C::kWarpK || warp == C::kWarpV) {
     // ---------------- TMA producers ----------------
@@ -262,6 +142,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       uint32_t phase = 1;  // parity of the slot's last release
       bool ok = true;
       while (ok && walk.next()) {
+        const int g = walk.item / np;
         for (int x = 0; x < walk.n; ++x) {
           if (issued >= NS && !mbar_wait_or_abort(bar(empty + slot), phase, abort_flag)) {
             fail();
@@ -272,7 +153,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           mbar_expect_tx(bar(full + slot), C::kTile);
 #pragma unroll
           for (int h2 = 0; h2 < D / 64; ++h2)
-            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, walk.g, (walk.j0 + x) * kRows, walk.s, bar(full + slot));
+            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, g, (walk.j0 + x) * kRows, walk.s, bar(full + slot));
           ++issued;
           if (++slot == NS) {
             slot = 0;
@@ -347,7 +228,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
             ++vit;
           }
         } else {
-          const bool two = R - walk.pair * 256 > kRows;
+          const int pair = walk.item % np;
+          const bool two = R - pair * 256 > kRows;
           ok = mbar_wait_or_abort(bar(C::B_QFULL), (uint32_t)seg & 1u, abort_flag) &&
                mbar_wait_or_abort(bar(C::B_QFULL + NT - 1), (uint32_t)seg & 1u, abort_flag) && wait_k();
           if (!ok) break;
@@ -406,8 +288,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     };
     while (ok && walk.next()) {
       const int64_t seq = walk.s;
+      const int g = walk.item / np, pair = walk.item - g * np;
       const int L = (int)walk.L;
-      const int base = walk.pair * (NT * kRows) + t * kRows;  // first query row of the tile
+      const int base = pair * (NT * kRows) + t * kRows;  // first query row of the tile
       const int nr = min(kRows, R - base);                     // rows of the tile (none: below 1)
       // Q rows of the tile; the last use of its buffer ended with the segment before
       if (nr > 0) {
@@ -419,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
           if (row < nr) {
             const int i = (base + row) / G, hg = (base + row) - i * G;
-            x = ld_nc_v4(q + ((seq * T + i) * H + walk.g * G + hg) * D + c * 8);
+            x = ld_nc_v4(q + ((seq * T + i) * H + g * G + hg) * D + c * 8);
           }
           *reinterpret_cast<uint4*>(smem + t * C::kTile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
         }
@@ -450,8 +333,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         const uint32_t ts = tmem + lanes + 128u * (uint32_t)buf;
         const int t0 = (walk.j0 + x) * kRows;
         const bool tail = t0 + kRows > L;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + buf), par, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
         if (tail && t == 0) {
-          // V rows behind the context: thread = row of the V tile
+          // V rows behind the context: thread = row of the V tile.  The scores are in, so the V tile two
+          // before has been multiplied and the wait below cannot take an earlier fill of the slot for this one.
           const int vs = vit % C::VS;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)(vit / C::VS) & 1u, abort_flag));
           if (!ok) break;
@@ -483,9 +370,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           fence_async_smem();
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + buf), par, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
         if (warp_rows) {
           uint32_t raw[4][32];
 #pragma unroll
@@ -558,6 +442,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           tmem_wait_st();
         }
+        // Two score buffers: these scores say only that the product before the last one is in.  The wait
+        // behind the segment's last tile can tell its product from that of the tile before alone, so
+        // that one is waited for here.
+        if (NT == 1 && x + 1 == walk.n && cnt > 0) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag));
+          if (!ok) break;
+        }
         tc_fence_before();
         mbar_arrive(bar(C::B_PREADY + buf));
       }
@@ -573,7 +464,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       }
       const bool whole = walk.whole();
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int64_t row = (seq * T + slot_i) * H + walk.g * G + (base + r - slot_i * G);
+      const int64_t row = (seq * T + slot_i) * H + g * G + (base + r - slot_i * G);
       const int64_t prow = ((int64_t)blockIdx.x * 2 + walk.slot()) * (NT * kRows) + t * kRows + r;
       const uint32_t any_odd = odd[0] | odd[1] | odd[2] | odd[3] | odd[4] | odd[5] | odd[6] | odd[7];
 #pragma unroll 1
@@ -593,7 +484,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int j = 0; j < T; ++j) {
             if (!((odd[j >> 5] >> (j & 31)) & 1u)) continue;
             if (parent ? !((tree.anc[slot_i][j >> 5] >> (j & 31)) & 1u) : j > slot_i) continue;
-            const uint32_t* vr = reinterpret_cast<const uint32_t*>(v + (((seq * n_kv + L + j) * Hkv) + walk.g) * D + c0);
+            const uint32_t* vr = reinterpret_cast<const uint32_t*>(v + (((seq * n_kv + L + j) * Hkv) + g) * D + c0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const uint32_t w = vr[i];
@@ -646,9 +537,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 constexpr int kMergeThreads = 256;
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kMergeThreads)
-    tree_attn_merge_kernel(Work work, const int32_t* __restrict__ kv_len, uint16_t* __restrict__ o,
-                           float* __restrict__ lse, int32_t* __restrict__ status, int batch, int T, int64_t n_kv, int H,
-                           int Hkv, int tile_rows, int grid) {
+    tree_attn_merge_kernel(Work work, uint16_t* __restrict__ o,
+                           float* __restrict__ lse, int batch, int T, int H, int Hkv, int tile_rows, int grid) {
   constexpr int NW = kMergeThreads / 32, LN = D / 4, PER = 32 / LN;  // lanes of a row, parts a warp takes at once
   __shared__ float sm_l[NW], sm_m[NW];
   __shared__ float4 sm_o[NW][32];
@@ -666,10 +556,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (tiles == 0) {
     if (SPLIT && warp != 0) return;
     if (sub == 0) *reinterpret_cast<uint2*>(o + row * D + 4 * c) = make_uint2(0u, 0u);
-    if (lane == 0) {
-      if (lse) lse[row] = -INFINITY;
-      if (status) atomicOr(status, kStatusBadIndex);
-    }
+    if (lane == 0 && lse) lse[row] = -INFINITY;
     return;
   }
   const int64_t units = total * Hkv * np, ctas = range_ctas(units, grid);
@@ -799,8 +686,8 @@ cudaError_t launch(const Shape& s, const void* q, const void* k, const void* v, 
   const bool split = items * 4 < ctas;
   const int rows = (int)s.n_q * s.H, per = split ? 1 : kMergeThreads / 32;
   return launch_after(split ? tree_attn_merge_kernel<D, true> : tree_attn_merge_kernel<D, false>,
-                      dim3((unsigned)((rows + per - 1) / per), (unsigned)s.batch), kMergeThreads, st, work, kv_len,
-                      static_cast<uint16_t*>(o), lse, status, s.batch, (int)s.n_q, s.n_kv, s.H, s.Hkv, NT * kRows, ctas);
+                      dim3((unsigned)((rows + per - 1) / per), (unsigned)s.batch), kMergeThreads, st, work,
+                      static_cast<uint16_t*>(o), lse, s.batch, (int)s.n_q, s.H, s.Hkv, NT * kRows, ctas);
 }
 
 }  // namespace

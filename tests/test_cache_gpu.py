@@ -177,6 +177,36 @@ def test_large_scores_and_small_rows(hs):
     check_tree(hs, x, 8, 2, 128, True)
 
 
+@pytest.mark.parametrize("Hk,T", [(16, 1), (4, 3)])
+def test_long_caches_of_a_batch(hs, Hk, T):
+    """Hundreds of key tiles in a row for every SM, heads and sequences ending inside the SMs' shares: every row
+    agrees with the definition, and with itself when the call is repeated."""
+    b, H, d, n_kv = 4, 16, 128, 24000
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    q, k, v = normal(b, T, H, d), normal(b, n_kv, Hk, d), normal(b, n_kv, Hk, d)
+    lens = torch.tensor([23990, 23000, 17001, 23808], dtype=torch.int32, device="cuda")
+    p = hs.params(b, T, n_kv, 128, 128, 4, 64, H, Hk, d)
+    first = hs.tree_attn(p, q, k, v, lens)
+    for _ in range(20):
+        assert all(torch.equal(x, y) for x, y in zip(first, hs.tree_attn(p, q, k, v, lens)))
+    for s in range(b):
+        L = int(lens[s])
+        z = torch.einsum("ihd,nhd->ihn", q[s].double(), k[s, :L + T].double().repeat_interleave(H // Hk, 1)) / d**0.5
+        at = torch.arange(L + T, device="cuda")
+        z.masked_fill_((at > L + torch.arange(T, device="cuda")[:, None])[:, None], -math.inf)
+        lse = torch.logsumexp(z, -1)
+        pr = (z - lse[..., None]).exp()
+        vv = v[s, :L + T].double().repeat_interleave(H // Hk, 1)
+        want, spread = torch.einsum("ihn,nhd->ihd", pr, vv), torch.einsum("ihn,nhd->ihd", pr, vv.abs())
+        dl = delta(d, 100.0 / d**0.5 * 3)  # sum |q_c k_c| of 128 pairs of normal values: below 300
+        close(first[1][s], lse.cpu(), dl + 2.0**-22 * lse.cpu().abs(), "lse")
+        close(first[0][s], want.cpu(), 2.0**-8 * want.cpu().abs() + 2 * dl * spread.cpu(), "o")
+
+
 def test_rising_scores(hs):
     """Every tile raises the maximum: keys grow along the cache in the query's own direction."""
     x = make_inputs(1, 8, 4, 2, 128, 2048, [2040], "tree", seed=4)
