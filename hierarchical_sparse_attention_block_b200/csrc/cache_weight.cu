@@ -254,16 +254,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int CH = D / 8;  // 16-byte chunks of a row
         uint8_t* qb = smem + b * C::kTile;
         const int total = ch.n * ch.pitch;  // buffer rows
-#pragma unroll 8
+        // all copies of the fill in flight at once (16 bytes each, CH threads a row)
         for (int e = lt; e < total * CH; e += kLoaders) {
           const int row = e / CH, x = e % CH, hd = row / ch.pitch, rr = row - hd * ch.pitch;
-          uint4 val = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < ch.rows) {
-            const int r = ch.row0 + rr, ci = r / G, slot = list[ci];
-            val = ld_nc_v4(q + ((seq * T + slot) * H + (ch.head + hd) * G + (r - ci * G)) * D + x * 8);
+          const uint16_t* src = q;
+          const bool held = rr < ch.rows;
+          if (held) {
+            const int r = ch.row0 + rr, ci = r / G;
+            src = q + ((seq * T + list[ci]) * H + (ch.head + hd) * G + (r - ci * G)) * D + x * 8;
           }
-          *reinterpret_cast<uint4*>(qb + (x >> 3) * kHalf + row * 128 + (((x & 7) ^ (row & 7)) << 4)) = val;
+          cp_async16(qb + (x >> 3) * kHalf + row * 128 + (((x & 7) ^ (row & 7)) << 4), src, held);
         }
+        cp_async_commit();
         for (int row = lt; row < total; row += kLoaders) {
           const int hd = row / ch.pitch, rr = row - hd * ch.pitch;
           Row out = {INFINITY, 0};
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           rows_of[b * kQRows + row] = out;
         }
+        cp_async_wait<0>();
         fence_async_smem();
         mbar_arrive(bar(C::B_QFULL + b));
       }

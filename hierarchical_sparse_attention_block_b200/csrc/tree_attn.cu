@@ -296,16 +296,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (nr > 0) {
         const int fill = (nr + 31) & ~31;  // the rows of warps that take part
         constexpr int CH = D / 8;          // 16-byte chunks of a row
-#pragma unroll 4
         for (int e = r; e < fill * CH; e += kRows) {
           const int row = e / CH, c = e % CH;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < nr) {
-            const int i = (base + row) / G, hg = (base + row) - i * G;
-            x = ld_nc_v4(q + ((seq * T + i) * H + g * G + hg) * D + c * 8);
-          }
-          *reinterpret_cast<uint4*>(smem + t * C::kTile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = x;
+          const bool held = row < nr;
+          const int i = (base + row) / G, hg = (base + row) - i * G;
+          cp_async16(smem + t * C::kTile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                     held ? q + ((seq * T + i) * H + g * G + hg) * D + c * 8 : q, held);
         }
+        cp_async_commit();
+        cp_async_wait<0>();
         fence_async_smem();
       }
       mbar_arrive(bar(C::B_QFULL + t));
