@@ -5,8 +5,8 @@
 // by radix, 8 bits a pass from the top, then one counting and one emitting sweep in row order.
 //
 // A cluster of up to 16 CTAs takes one sequence, a contiguous part of its rows each, so that a single
-// long cache is not left to one SM; the parts stay in shared memory where they fit (48K rows a CTA),
-// else each sweep reads them again (L2).  A pass counts into 32 copies of the 256 counters, copy =
+// long cache is not left to one SM; the first 47K rows of a part stay in shared memory, each sweep reads
+// the others again (L2).  A pass counts into 32 copies of the 256 counters, copy =
 // lane: the atomics of a warp never meet, whatever the weights' distribution (accumulated weights
 // share few exponents, equal ones are frequent).  The CTAs exchange their 256 sums through
 // distributed shared memory.  The bound is the sweeps' latency, not the 4 bytes a row.
@@ -21,16 +21,20 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kUnroll = 16;  // keys a thread reads at once
 constexpr int kMaxCluster = 16;
-constexpr int kStaged = 48 * 1024;  // rows a CTA holds in shared memory
+constexpr int kStaged = 47 * 1024;  // rows a CTA holds in shared memory
 
 struct Shared {
   uint32_t copies[256][32];  // counters of the running pass, copy = lane
   uint32_t sums[2][256];     // this CTA's sums, of the passes in turn (read by the whole cluster)
+  uint32_t totals[256];      // the cluster's
   uint32_t counts[2];        // this CTA's keys above and at the threshold
   uint32_t warp_gt[kWarps], warp_eq[kWarps];
   uint32_t digit, above, at;
 };
+
+static_assert(sizeof(Shared) + 4 * kStaged <= 227 * 1024, "shared memory budget");
 
 // Order-preserving key of a weight: every NaN above +inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -75,8 +79,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t b0 = all * rank / nc;
   const int n = (int)(all * (rank + 1) / nc - b0);
   const float* w = weight + seq * n_kv + n_first + b0;
-  const bool staged = n <= kStaged;
-  auto key = [&](int i) { return staged ? held[i] : weight_key(w[i]); };
+  const int staged = min(n, kStaged);  // the first rows' keys stay here
+  auto key = [&](int i) { return i < staged ? held[i] : weight_key(w[i]); };
 
   uint32_t prefix = 0, mask = 0, krem = (uint32_t)K;
   bool tie = true;  // of the keys equal to the prefix under the mask the first krem are taken, else all
@@ -85,32 +89,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = tid; i < 256 * 32; i += kThreads) (&sm.copies[0][0])[i] = 0;
     __syncthreads();
     if (pass == 0) {
-      for (int i0 = 0; i0 < n; i0 += 8 * kThreads) {
-        float x[8];
+      for (int i0 = 0; i0 < n; i0 += kUnroll * kThreads) {
+        float x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
           const int i = i0 + u * kThreads + tid;
           x[u] = i < n ? w[i] : 0.f;
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
           const int i = i0 + u * kThreads + tid;
           if (i >= n) continue;
           const uint32_t k = weight_key(x[u]);
-          if (staged) held[i] = k;
+          if (i < staged) held[i] = k;
           atomicAdd(&sm.copies[k >> 24][lane], 1u);
         }
       }
     } else {
-      for (int i0 = 0; i0 < n; i0 += 8 * kThreads) {
-        uint32_t x[8];
+      for (int i0 = 0; i0 < n; i0 += kUnroll * kThreads) {
+        uint32_t x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kUnroll; ++u) {
           const int i = i0 + u * kThreads + tid;
           x[u] = i < n ? key(i) : ~prefix;
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kUnroll; ++u)
           if ((x[u] & mask) == prefix) atomicAdd(&sm.copies[(x[u] >> shift) & 255u][lane], 1u);
       }
     }
@@ -124,15 +128,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mine[bin] = c;
     }
     cluster.sync();
-    if (warp == 0) {
-      // the whole cluster's counts of digits 255 - 8 lane - b, from the highest; the digit that holds
-      // the krem-th largest key
-      uint32_t c[8] = {0, 0, 0, 0, 0, 0, 0, 0}, tot = 0;
-      for (int r = 0; r < nc; ++r) {
-        const uint32_t* theirs = cluster.map_shared_rank(mine, r);
+    if (tid < 256) {
+      uint32_t c[kMaxCluster];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) c[b] += theirs[255 - 8 * lane - b];
-      }
+      for (int r = 0; r < kMaxCluster; ++r) c[r] = r < nc ? cluster.map_shared_rank(mine, r)[tid] : 0u;
+#pragma unroll
+      for (int r = 1; r < kMaxCluster; ++r) c[0] += c[r];
+      sm.totals[tid] = c[0];
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // digits 255 - 8 lane - b, from the highest; the digit that holds the krem-th largest key
+      uint32_t c[8], tot = 0;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) c[b] = sm.totals[255 - 8 * lane - b];
 #pragma unroll
       for (int b = 0; b < 8; ++b) tot += c[b];
       uint32_t incl = tot;
@@ -168,15 +177,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int span = ((n + kWarps - 1) / kWarps + 31) & ~31;
   const int w0 = min(warp * span, n), w1 = min(w0 + span, n);
   uint32_t gt = 0, eq = 0;
-  for (int c0 = w0; c0 < w1; c0 += 128) {
-    uint32_t x[4];
+  for (int c0 = w0; c0 < w1; c0 += 256) {
+    uint32_t x[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const int i = c0 + 32 * u + lane;
       x[u] = i < w1 ? key(i) : 0u;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const bool in = c0 + 32 * u + lane < w1;
       gt += in && (x[u] & mask) > prefix;
       eq += in && (x[u] & mask) == prefix;
@@ -214,15 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t place = n_first + above + min(ties, quota);
   const uint32_t below = (1u << lane) - 1u;
   const int32_t row0 = (int32_t)(n_first + b0);
-  for (int c0 = w0; c0 < w1; c0 += 128) {
-    uint32_t x[4];
+  for (int c0 = w0; c0 < w1; c0 += 256) {
+    uint32_t x[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const int i = c0 + 32 * u + lane;
       x[u] = i < w1 ? key(i) : 0u;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const int i = c0 + 32 * u + lane;
       const bool is_eq = i < w1 && (x[u] & mask) == prefix;
       const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);

@@ -10,17 +10,18 @@
 // row of weights up in registers: no sum crosses threads, and its order is fixed.  K is read once:
 // bound by HBM for few rows, by the exponentials (16 a clock and SM) from about 128 rows a KV head.
 //
-// Work: a unit is one key tile of one sequence for a group of KV heads (all of them, unless the
-// call has fewer key tiles than SMs: then the heads are split, each group's sums go to the workspace
-// and cache_weight_join_kernel adds them in order).  A CTA takes its range two key tiles at a time,
-// one for each of its two readout groups, and streams their K heads through a ring; the query rows
-// of as many heads as fit 128 rows stay in shared memory for all key tiles of the segment (two
-// buffers: the next heads' rows arrive meanwhile).  A head with more than 128 rows takes several
-// passes over the segment's keys.
+// Work: a unit is one key tile of one sequence for a group of KV heads: as many heads as have their
+// query rows in one buffer of 128 (fewer heads where the call has fewer units than SMs).  So a CTA
+// keeps its query rows for all key tiles of a segment; each group's sums (4 bytes a key against its
+// heads' 2 d bytes of K) go to the workspace and cache_weight_join_kernel adds them in order.  A CTA
+// takes its range two key tiles at a time, one for each of its two readout groups.  A head with more
+// than 128 rows takes several passes over the segment's keys.
 // Roles (448 threads): warps 0-3 and 4-7 readout groups, thread = key; warps 8-11 the counted slots,
 // the tree and the query rows (a gather: the counted slots lie anywhere); one thread each for the K
 // loads (TMA) and the MMAs.  Every wait is bounded (1 s): a timeout sets status bit 1.
 #include <math.h>
+
+#include <algorithm>
 
 #include "attn_math.cuh"
 #include "cache_walk.cuh"
@@ -43,10 +44,10 @@ constexpr int kWarpQ = 8, kWarpK = 12, kWarpMMA = 13;
 constexpr uint32_t kTmemCols = 512;  // score buffer b at 128 b; readout group e uses buffers 2 e, 2 e + 1
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What a query row of a buffer adds: lse in the log2 domain (+inf: nothing) and its slot.
-struct Row {
-  float lse2;
-  int slot;
+// What the query rows of a buffer add: minus their LSE in the log2 domain (-inf: nothing), their slots.
+struct Rows {
+  float nlse2[kQRows];
+  int16_t slot[kQRows];
 };
 
 template <int D>
@@ -55,8 +56,8 @@ struct Cfg {
   static constexpr int KS = D == 64 ? 8 : 4;  // K ring
   static constexpr int K_OFF = 2 * kTile;     // Q buffer b at b * kTile (kQRows rows)
   static constexpr int TREE_OFF = K_OFF + KS * kTile;
-  static constexpr int ROW_OFF = (TREE_OFF + (int)sizeof(DraftTree) + 15) / 16 * 16;  // Row [2][kQRows]
-  static constexpr int LIST_OFF = ROW_OFF + 2 * kQRows * (int)sizeof(Row);            // counted slots: int16 [kMaxDraft]
+  static constexpr int ROW_OFF = (TREE_OFF + (int)sizeof(DraftTree) + 15) / 16 * 16;  // Rows [2]
+  static constexpr int LIST_OFF = ROW_OFF + 2 * (int)sizeof(Rows);                    // counted slots: int16 [kMaxDraft]
   static constexpr int BAR_OFF = LIST_OFF + 2 * kMaxDraft;
   enum : int {
     B_KFULL = 0,             // [KS]
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) { return sb + (uint32_t)C::BAR_OFF + 8u * (uint32_t)i; };
   DraftTree& tree = *reinterpret_cast<DraftTree*>(smem + C::TREE_OFF);
-  Row* rows_of = reinterpret_cast<Row*>(smem + C::ROW_OFF);
+  Rows* rows_of = reinterpret_cast<Rows*>(smem + C::ROW_OFF);
   int16_t* list = reinterpret_cast<int16_t*>(smem + C::LIST_OFF);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   uint32_t* tmem_slot = misc;
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     if (status) atomicOr(status, kStatusTimeout);
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == kWarpMMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols));
@@ -266,16 +268,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async16(qb + (x >> 3) * kHalf + row * 128 + (((x & 7) ^ (row & 7)) << 4), src, held);
         }
         cp_async_commit();
-        for (int row = lt; row < total; row += kLoaders) {
-          const int hd = row / ch.pitch, rr = row - hd * ch.pitch;
-          Row out = {INFINITY, 0};
+        Rows& rows = rows_of[b];
+        if (lt < total) {
+          const int hd = lt / ch.pitch, rr = lt - hd * ch.pitch;
+          float nl = -INFINITY;
+          int slot = 0;
           if (rr < ch.rows) {
             const int r = ch.row0 + rr, ci = r / G;
-            out.slot = list[ci];
-            const float l = lse[(seq * T + out.slot) * H + (ch.head + hd) * G + (r - ci * G)];
-            out.lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
+            slot = list[ci];
+            const float l = lse[(seq * T + slot) * H + (ch.head + hd) * G + (r - ci * G)];
+            nl = l == -INFINITY ? -INFINITY : l * -kLog2e;
           }
-          rows_of[b * kQRows + row] = out;
+          rows.nlse2[lt] = nl;
+          rows.slot[lt] = (int16_t)slot;
         }
         cp_async_wait<0>();
         fence_async_smem();
@@ -405,25 +410,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + 2 * e + buf), (uint32_t)(got >> 1) & 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const Row* rows = rows_of + qb * kQRows + hd * ch.pitch;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int c0 = 0; c0 < ch.rows; c0 += 16) {
-              uint32_t s[16];
+            const Rows& rows = rows_of[qb];
+            const int first = hd * ch.pitch;
+            const float2 qs2 = {qscale, qscale};
+            float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            for (int c0 = 0; c0 < ch.pitch; c0 += 32) {
+              // 32 columns (the last block may reach behind the pitch, within the score buffer)
+              uint32_t s[32];
               __syncwarp();  // the load takes the whole warp
-              tmem_ld<16>(ts + 128u * (uint32_t)buf + (uint32_t)c0, s);
+              tmem_ld32_issue(ts + 128u * (uint32_t)buf + (uint32_t)c0, s);
+              tmem_wait_ld(s);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const Row row = rows[c0 + i];
-                bool see = row.lse2 < INFINITY || row.lse2 != row.lse2;  // padding and rows that count nothing: +inf
-                if (tail && j >= 0)
-                  see = see && (parent ? j < T && ((tree.anc[row.slot][j >> 5] >> (j & 31)) & 1u) : j <= row.slot);
-                const float p = fast_exp2(fmaf(__uint_as_float(s[i]), qscale, -row.lse2));
-                acc[i & 3] += see ? p : 0.f;
+              for (int h = 0; h < 2; ++h) {
+                if (c0 + 16 * h >= ch.pitch) break;
+                float nl[16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  *reinterpret_cast<float4*>(nl + i) = *reinterpret_cast<const float4*>(rows.nlse2 + first + c0 + 16 * h + i);
+                if (c0 + 16 * h + 16 <= ch.rows && !tail) {
+                  bool none = false;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) none = none || nl[i] == -INFINITY;
+                  if (!none) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const float2 x = ffma2(make_float2(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])),
+                                             qs2, make_float2(nl[2 * i], nl[2 * i + 1]));
+                      acc[i & 1] = fadd2(acc[i & 1], make_float2(fast_exp2(x.x), fast_exp2(x.y)));
+                    }
+                    continue;
+                  }
+                }
+                // padding, rows that add nothing (-inf), and what a drafted row is not seen by
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  bool see = nl[i] != -INFINITY;
+                  if (tail && j >= 0) {
+                    const int slot = rows.slot[first + c0 + 16 * h + i];
+                    see = see && (parent ? j < T && ((tree.anc[slot][j >> 5] >> (j & 31)) & 1u) : j <= slot);
+                  }
+                  const float p = fast_exp2(fmaf(__uint_as_float(s[16 * h + i]), qscale, nl[i]));
+                  acc[0].x += see ? p : 0.f;
+                }
               }
             }
             tc_fence_before();
             mbar_arrive(bar(C::B_SFREE + 2 * e + buf));
-            sum += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            acc[0] = fadd2(acc[0], acc[1]);
+            sum += acc[0].x + acc[0].y;
           }
           if (ok) add(c, t, sum);
         }
@@ -446,21 +480,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256)
     cache_weight_join_kernel(const float* __restrict__ part, const int32_t* __restrict__ kv_len,
                              float* __restrict__ weight, int batch, int T, int64_t n_kv, int groups) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t seq = blockIdx.y, L = context_len(kv_len, seq, T, n_kv);
-  if (L < 0) return;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < L + T; t += (int64_t)gridDim.x * 256) {
-    float sum = t < L ? weight[seq * n_kv + t] : 0.f;
-    for (int g = 0; g < groups; ++g) sum += part[((int64_t)g * batch + seq) * n_kv + t];
-    weight[seq * n_kv + t] = sum;
-  }
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (L < 0 || t >= L + T) return;
+  float sum = t < L ? weight[seq * n_kv + t] : 0.f;
+#pragma unroll 8
+  for (int g = 0; g < groups; ++g) sum += part[((int64_t)g * batch + seq) * n_kv + t];
+  weight[seq * n_kv + t] = sum;
 }
 
-// KV-head groups: one, unless the key tiles alone leave SMs idle.
+// KV-head groups: of as many heads as have their query rows in one buffer, and at least as many
+// groups as give every SM a unit.
 int head_groups(const Shape& s) {
+  const int64_t R = s.n_q * (s.H / s.Hkv), pitch = (R + 15) / 16 * 16;
+  const int64_t heads = R > kQRows ? 1 : kQRows / pitch;
   const int64_t tiles = (int64_t)s.batch * ((s.n_kv + kKeys - 1) / kKeys);
-  if (tiles >= kMaxCtas) return 1;
-  const int64_t g = (kMaxCtas + tiles - 1) / tiles;
-  return (int)(g < s.Hkv ? g : s.Hkv);
+  const int64_t g = std::max((s.Hkv + heads - 1) / heads, (kMaxCtas + tiles - 1) / tiles);
+  return (int)std::min<int64_t>(g, s.Hkv);
 }
 
 template <int D>
@@ -479,12 +516,9 @@ cudaError_t launch(const Shape& s, const void* q, const void* k, const int32_t* 
       s.H, s.Hkv, groups, s.scale * kLog2e);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (groups > 1) {
-    const int64_t want = (s.n_kv + 255) / 256;
-    cache_weight_join_kernel<<<dim3((unsigned)want, (unsigned)s.batch), 256, 0, st>>>(part, kv_len, weight, s.batch,
-                                                                                      (int)s.n_q, s.n_kv, groups);
-    e = cudaGetLastError();
-  }
+  if (groups > 1)
+    e = launch_after(cache_weight_join_kernel, dim3((unsigned)((s.n_kv + 255) / 256), (unsigned)s.batch), 256, st, part,
+                     kv_len, weight, s.batch, (int)s.n_q, s.n_kv, groups);
   return e;
 }
 

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const float M = warp_max(m);
   l = warp_sum(l * (m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M)));
   float4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (int p = p0 + step * sub; p < n; p += step * PER) {
     const int64_t pr = part_row(p);
     const float2 ml = work.part_ml[pr];
@@ -647,22 +647,6 @@ Layout layout(const Shape& s, bool with_weight) {
   return L;
 }
 
-// A launch that may be scheduled while the kernel before it drains; that kernel's results are
-// waited for inside (griddepcontrol.wait).
-template <class... P, class... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-}
-
 template <int D, int NT>
 cudaError_t launch(const Shape& s, const void* q, const void* k, const void* v, const int32_t* kv_len,
                    const int32_t* parent, void* o, float* lse, Work work, int32_t* status, cudaStream_t st) {
@@ -682,7 +666,9 @@ cudaError_t launch(const Shape& s, const void* q, const void* k, const void* v, 
       s.scale * kLog2e);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool split = items * 4 < ctas;
+  // a CTA per row where an item's parts are many, or where the rows are so few that one wave of CTAs
+  // takes them all
+  const bool split = items * 16 < ctas || (items * 4 < ctas && s.n_query * s.H <= 8 * kMaxCtas);
   const int rows = (int)s.n_q * s.H, per = split ? 1 : kMergeThreads / 32;
   return launch_after(split ? tree_attn_merge_kernel<D, true> : tree_attn_merge_kernel<D, false>,
                       dim3((unsigned)((rows + per - 1) / per), (unsigned)s.batch), kMergeThreads, st, work,
