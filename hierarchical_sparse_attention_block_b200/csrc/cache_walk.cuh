@@ -31,21 +31,23 @@ struct Walk {
   int64_t n_kv, u, u1, first;  // first: the range's begin
   int64_t P;                   // key tiles of the sequences before s
   int64_t L, tiles;
-  int s, T, per_seq;           // per_seq: items of a sequence
+  int64_t L_next;              // of sequence s + 1: its load is long over when the walk gets there
+  int s, T, per_seq, batch;    // per_seq: items of a sequence
   // the segment: key tiles [j0, j0 + n) of the item
   int item, j0, n;
   int64_t start;
 
-  __device__ void at(int seq) {
+  __device__ void at(int seq, int64_t len) {
     s = seq;
-    L = context_len(kv_len, seq, T, n_kv);
+    L = len;
     tiles = key_tiles(L, T);
+    if (seq + 1 < batch) L_next = context_len(kv_len, seq + 1, T, n_kv);
   }
   __device__ bool next() {
     if (u >= u1) return false;
     while (u >= (P + tiles) * per_seq) {
       P += tiles;
-      at(s + 1);
+      at(s + 1, L_next);
     }
     const int64_t rel = u - P * per_seq;
     item = (int)(rel / tiles);
@@ -104,6 +106,7 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
   walk.n_kv = n_kv;
   walk.T = T;
   walk.per_seq = per_seq;
+  walk.batch = batch;
   walk.u = walk.first = busy ? range_begin(blockIdx.x, units, ctas) : 0;
   walk.u1 = busy ? range_begin(blockIdx.x + 1, units, ctas) : 0;
   if (busy && walk.u >= before * per_seq && walk.u < (before + mine) * per_seq) {
@@ -129,7 +132,7 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
   __syncthreads();
   if (busy) {
     walk.P = sm.found[1];
-    walk.at((int)sm.found[0]);
+    walk.at((int)sm.found[0], context_len(kv_len, (int)sm.found[0], T, n_kv));
   }
   return walk;
 }
@@ -152,10 +155,11 @@ __device__ __forceinline__ uint32_t chain_word(int i, int off) {
 // A launch that may be scheduled while the kernel before it drains; that kernel's results are
 // waited for inside (griddepcontrol.wait).
 template <class... P, class... A>
-inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, int smem, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

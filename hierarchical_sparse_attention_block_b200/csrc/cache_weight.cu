@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_init_fence();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   tc_fence_before();
   Walk walk = walk_begin<kThreads>(kv_len, n_kv, T, batch, groups,
                                    *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), nullptr, status);
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             above = e[x];
-            if (!parent || tree.up[e[x]] == kRoot) {
+            if (!parent || tree.end[e[x]] == kRoot) {
               keep |= 1u << x;
               ++kept;
             }
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int n = 0;
           for (int i0 = 0; i0 < T; i0 += 32) {
             const int i = i0 + lane;
-            const bool c = i < T && (!parent || tree.up[i] == kRoot);
+            const bool c = i < T && (!parent || tree.end[i] == kRoot);
             const uint32_t b = __ballot_sync(0xFFFFFFFFu, c);
             if (c) list[n + __popc(b & ((1u << lane) - 1u))] = (int16_t)i;
             n += __popc(b);
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
       bool ok = true;
+      const uint64_t policy = l2_evict_first();
       int seg = 0, issued = 0;
       while (ok && walk.next()) {
         ok = mbar_wait_or_abort(bar(C::B_SEGFULL), (uint32_t)seg & 1u, abort_flag);
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h2 = 0; h2 < D / 64; ++h2)
                   tma_load_4d(dst + h2 * kHalf, &map_k, 64 * h2, ch.head + hd, (walk.j0 + x + e) * kKeys, walk.s,
-                              bar(C::B_KFULL + s));
+                              bar(C::B_KFULL + s), policy);
                 ++issued;
               }
         }
@@ -511,13 +513,12 @@ cudaError_t launch(const Shape& s, const void* q, const void* k, const int32_t* 
   if (e != cudaSuccess) return e;
   const int groups = head_groups(s);
   const int64_t most = (int64_t)s.batch * groups * ((s.n_kv + kKeys - 1) / kKeys);
-  cache_weight_kernel<D><<<(unsigned)(most < kMaxCtas ? most : kMaxCtas), kThreads, Cfg<D>::kSmem, st>>>(
-      mk, static_cast<const uint16_t*>(q), kv_len, parent, path, lse, weight, part, status, s.batch, (int)s.n_q, s.n_kv,
-      s.H, s.Hkv, groups, s.scale * kLog2e);
-  e = cudaGetLastError();
+  e = launch_after(cache_weight_kernel<D>, dim3((unsigned)(most < kMaxCtas ? most : kMaxCtas)), kThreads, st,
+                   Cfg<D>::kSmem, mk, static_cast<const uint16_t*>(q), kv_len, parent, path, lse, weight, part, status,
+                   s.batch, (int)s.n_q, s.n_kv, s.H, s.Hkv, groups, s.scale * kLog2e);
   if (e != cudaSuccess) return e;
   if (groups > 1)
-    e = launch_after(cache_weight_join_kernel, dim3((unsigned)((s.n_kv + 255) / 256), (unsigned)s.batch), 256, st, part,
+    e = launch_after(cache_weight_join_kernel, dim3((unsigned)((s.n_kv + 255) / 256), (unsigned)s.batch), 256, st, 0, part,
                      kv_len, weight, s.batch, (int)s.n_q, s.n_kv, groups);
   return e;
 }

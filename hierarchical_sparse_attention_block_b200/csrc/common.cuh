@@ -59,6 +59,9 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
+// Bring the line of p into the L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Tokens of block `blk` that a query at position p sees: [blk*B, min(blk*B+B, p+1)).
 // (p < n_kv always, so the sequence end never cuts further.)
 __device__ __forceinline__ int visible_len(int64_t blk, int B, int64_t p) {

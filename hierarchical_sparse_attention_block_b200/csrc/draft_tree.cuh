@@ -15,66 +15,49 @@ __device__ __forceinline__ int64_t context_len(const int32_t* kv_len, int64_t se
 }
 
 // One sequence's tree in shared memory.
-struct DraftTree {
+struct alignas(16) DraftTree {
   uint32_t anc[kMaxDraft][kDraftWords];  // bit j of row i: slot j is slot i or one of its ancestors
-  int16_t up[kMaxDraft];                 // slot the walk stands at; kRoot, kEmpty at its end
+  int16_t parent[kMaxDraft];             // kRoot, kEmpty or the slot before
+  int16_t end[kMaxDraft];                // where the walk up from the slot ends: kRoot, kEmpty
 };
 constexpr int kRoot = -1, kEmpty = -2;
 
-// Fills `t` from parent[0 .. T) (null: a chain) with NT threads, tid of each; sync() is a barrier
-// over them.  A slot is a token iff t.up[i] == kRoot afterwards; the rows of empty slots are 0.  Returns
-// whether this thread saw a parent that is no parent, no root and no empty mark.
-// Each round joins every slot's set with the set of the slot its walk has reached and doubles the
-// walk's step, so ceil(log2 T) rounds reach the root from any depth.
+// Fills `t` from parent[0 .. T) with NT threads, tid of each; sync() is a barrier over them, the last
+// thing done.  A slot is a token iff t.end[i] == kRoot; the rows of empty slots are 0.  Returns whether
+// this thread saw a parent that is no parent, no root and no empty mark.  Every slot walks up to its
+// root by itself (a parent lies in front of its child, so the walk ends): as many steps in shared
+// memory as the tree is deep, and two barriers.
 template <int NT, class Sync>
 __device__ bool draft_tree_build(DraftTree& t, const int32_t* parent, int T, int tid, Sync sync) {
-  constexpr int kPer = (kMaxDraft + NT - 1) / NT;
-  const int nw = (T + 31) / 32;
   bool bad = false;
   for (int i = tid; i < T; i += NT) {
-    if (parent == nullptr) {
-      for (int w = 0; w < kDraftWords; ++w) {
-        const int hi = i - 32 * w;  // bits 0 .. hi of word w
-        t.anc[i][w] = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
-      }
-      t.up[i] = kRoot;
-      continue;
-    }
     const int p = parent[i];
     const bool ok = p >= -1 && p < i;
-    bad = bad || (!ok && p != -2);
-    for (int w = 0; w < kDraftWords; ++w) t.anc[i][w] = w == (i >> 5) ? 1u << (i & 31) : 0u;
-    t.up[i] = (int16_t)(ok ? p : kEmpty);
+    bad = bad || (!ok && p != kEmpty);
+    t.parent[i] = (int16_t)(ok ? p : kEmpty);
+    uint4* row = reinterpret_cast<uint4*>(t.anc[i]);
+    row[0] = row[1] = make_uint4(0u, 0u, 0u, 0u);
   }
   sync();
-  if (parent == nullptr) return false;
-  for (int reach = 1; reach < T; reach *= 2) {
-    // the sets and steps of this round are read before any of them is written
-    uint32_t set[kPer][kDraftWords];
-    int step[kPer];
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      const int i = tid + c * NT;
-      const int j = i < T ? t.up[i] : kRoot;
-      step[c] = j >= 0 ? t.up[j] : j;
-#pragma unroll
-      for (int w = 0; w < kDraftWords; ++w) set[c][w] = j >= 0 && w < nw ? t.anc[j][w] : 0u;
+  for (int i = tid; i < T; i += NT) {
+    int j = i, word = i >> 5;
+    uint32_t bits = 0;
+    while (j >= 0) {
+      if ((j >> 5) != word) {
+        t.anc[i][word] = bits;
+        bits = 0;
+        word = j >> 5;
+      }
+      bits |= 1u << (j & 31);
+      j = t.parent[j];
     }
-    sync();
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      const int i = tid + c * NT;
-      if (i >= T) continue;
-      t.up[i] = (int16_t)step[c];
-#pragma unroll
-      for (int w = 0; w < kDraftWords; ++w)
-        if (w < nw) t.anc[i][w] |= set[c][w];
+    t.anc[i][word] = bits;
+    t.end[i] = (int16_t)j;
+    if (j != kRoot) {
+      uint4* row = reinterpret_cast<uint4*>(t.anc[i]);
+      row[0] = row[1] = make_uint4(0u, 0u, 0u, 0u);
     }
-    sync();
   }
-  for (int i = tid; i < T; i += NT)
-    if (t.up[i] != kRoot)
-      for (int w = 0; w < nw; ++w) t.anc[i][w] = 0u;
   sync();
   return bad;
 }

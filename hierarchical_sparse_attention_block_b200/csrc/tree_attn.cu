@@ -16,19 +16,29 @@
 // SM.  An item that one CTA holds whole is written by it; the others leave (max, sum, unnormalised
 // output) per range in the workspace, merged by tree_attn_merge_kernel.
 //
-// Roles of a CTA (NT row tiles): warps 0 .. 4 NT - 1 softmax and output, one thread per query row
-// (TMEM lane = row); then one thread each for the K loads (TMA), the MMAs (tcgen05) and the V loads.
-// One row tile: two score buffers take the key tiles in turn, so the next tile's scores are formed
-// while this one's weights are.  Two row tiles: each has its score buffer, and the two alternate.
-// Scores and weights share columns of tensor memory: a row's 128 scores are read, and its weights
-// written over them as two bf16 numbers each (w = hi + lo to 16 significant bits: with one bf16 the
-// weights' rounding would equal the output's own), the A operands of two products with V.
+// Roles of a CTA: two softmax groups of four warps, one thread per query row (TMEM lane = row); then
+// one thread each for the K loads (TMA), the MMAs (tcgen05) and the V loads.  Two row tiles: each
+// group has its tile.  One row tile: the groups take the key tiles in turn, each with its own running
+// max, sum and output, joined at the segment's end; a group's softmax takes longer than a tile's
+// bytes, two side by side do not.  Up to 64 query rows (32) the tile holds them two (four) times, and
+// a warp forms the weights of half (a quarter) of the tile's keys for its copy, again with its own max
+// and sum: a row's 128 exponentials in one thread are what a group's time goes to.  Either way a
+// group's scores of the next tile follow the product with its weights of this one, and one group's
+// products run while the other's weights are formed.
+// Scores and weights share columns of tensor memory: a row's scores are read 32 at a time, and its
+// weights written over them.  Up to 64 query rows, where the tensor cores have time, a weight enters as
+// two bf16 numbers (w = hi + lo to 16 significant bits), the A operands of two products with V.  With
+// more it is one: rounding the weights to 8 bits then moves an output of n comparable weights by about
+// as much as its own rounding to bf16 does, and the second product would cost up to a quarter of the
+// call (16 x 32K rows, 128 query rows a KV head: 210 us with it, 161 without).
 //
 // Rows that a slot does not see get weight 0 by a bit mask in the key tiles from L on; there, V rows
 // that no token holds are zeroed in shared memory, and values that are no finite numbers are taken out
 // and added, at the end, to the rows that see them (0 x inf would reach the others).
 // Every wait is bounded (1 s): a timeout sets status bit 1 and the CTA stops.
 #include <math.h>
+
+#include <type_traits>
 
 #include "attn_math.cuh"
 #include "cache_walk.cuh"
@@ -48,26 +58,32 @@ constexpr int kHalf = kRows * 128;  // 64 columns of 128 rows of 16-bit values: 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kSoftmax = 256;  // two groups
+constexpr int kThreads = kSoftmax + 96;
+constexpr int kWarpK = 8, kWarpMMA = 9, kWarpV = 10;
+// Tensor memory: scores / weights of group t at 128 t, its output at col_o(t).
+__host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * (uint32_t)t; }
+
+// NT: row tiles of an item.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kSoftmax = 128 * NT;
-  static constexpr int kThreads = kSoftmax + 96;
-  static constexpr int kWarpK = 4 * NT, kWarpMMA = kWarpK + 1, kWarpV = kWarpK + 2;
   static constexpr int kTile = kHalf * (D / 64);
   // ring slots of K and of V: what 227 KB hold beside Q and the tree
-  static constexpr int KS = D == 64 ? 4 : NT == 1 ? 3 : 2, VS = D == 64 ? 4 : 2;
+  static constexpr int KS = D == 64 ? 5 : NT == 1 ? 3 : 2, VS = D == 64 ? 4 : 2;
   static constexpr int K_OFF = NT * kTile, V_OFF = K_OFF + KS * kTile, TREE_OFF = V_OFF + VS * kTile;
-  static constexpr int BAR_OFF = (TREE_OFF + (int)sizeof(DraftTree) + 15) / 16 * 16;
+  static constexpr int JOIN_OFF = (TREE_OFF + (int)sizeof(DraftTree) + 15) / 16 * 16;  // float2 [2][kRows]
+  static constexpr int BAR_OFF = JOIN_OFF + 2 * kRows * (int)sizeof(float2);
   enum : int {
-    B_QFULL = 0,               // [NT]
-    B_KFULL = B_QFULL + NT,    // [KS]
+    B_QFULL = 0,
+    B_KFULL,                   // [KS]
     B_KEMPTY = B_KFULL + KS,   // [KS]
     B_VFULL = B_KEMPTY + KS,   // [VS]
     B_VEMPTY = B_VFULL + VS,   // [VS]
-    B_SFULL = B_VEMPTY + VS,   // [2]: per score buffer
+    B_SFULL = B_VEMPTY + VS,   // [2]: per group
     B_PREADY = B_SFULL + 2,    // [2]
-    B_PFREE = B_PREADY + 2,    // [NT]
-    B_SYNC = B_PFREE + NT,     // the softmax warps among themselves
+    B_PFREE = B_PREADY + 2,    // [2]
+    B_SYNC = B_PFREE + 2,      // the softmax warps among themselves
+    B_GO,                      // the first segment's query rows are asked for
     B_DRAIN,
     kNBar
   };
@@ -75,22 +91,24 @@ struct Cfg {
   static constexpr int MISC_OFF = WALK_OFF + (int)sizeof(WalkShared<kThreads>);
   static constexpr int kSmem = MISC_OFF + 4 * (2 + 2 * kDraftWords) + 1024;  // + slack for the 1024-byte alignment
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + 128u * (uint32_t)t; }
 };
 
 // What the CTAs share with the merge: the unit ranges and the partial results.
 struct Work {
   int64_t* prefix;  // [b + 1] key tiles of the sequences before; the total at the end
-  float* part_o;    // [cta][2][NT * 128][D]
-  float2* part_ml;  // [cta][2][NT * 128]: max (log2 domain), sum
+  float4* part_o;   // [cta][2][D / 4][NT * 128]: four columns of a row; neighbours are rows
+  float2* part_ml;  // [cta][2][NT * 128]: max (log2 domain), sum; (+inf, 0): the row's slot is empty
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+template <int D, int NT, int REP>
+__global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const uint16_t* __restrict__ q, const uint16_t* __restrict__ v,
                      const int32_t* __restrict__ kv_len, const int32_t* __restrict__ parent, uint16_t* __restrict__ o,
-                     float* __restrict__ lse, Work work, int32_t* __restrict__ status, int batch, int T, int64_t n_kv, int H, int Hkv, float qscale) {
+                     float* __restrict__ lse, float* __restrict__ scores, int64_t score_stride, Work work,
+                     int32_t* __restrict__ status, int batch, int T, int64_t n_kv, int H, int Hkv, float qscale) {
+  static_assert(NT == 1 || REP == 1, "copies of the rows are for one row tile");
+  constexpr bool LO = REP > 1;  // weights as two bf16 numbers
   using C = Cfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -108,39 +126,43 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == C::kWarpMMA) {
+  if (warp == kWarpMMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
     for (int i = 0; i < C::kNBar; ++i) {
-      const bool soft = (i >= C::B_PREADY && i < C::B_PFREE) || (i >= C::B_QFULL && i < C::B_KFULL);
-      mbar_init(bar(i), soft ? kRows : i == C::B_SYNC ? C::kSoftmax : 1);
+      const bool group = i >= C::B_PREADY && i < C::B_PFREE;
+      mbar_init(bar(i), group ? kRows : i == C::B_SYNC || i == C::B_QFULL || i == C::B_GO ? kSoftmax : 1);
     }
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (tid < 2 * kDraftWords) odd_rows[tid] = 0u;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   const int G = H / Hkv, R = T * G, np = (R + NT * kRows - 1) / (NT * kRows);  // items: (KV head, row-tile pair)
   tc_fence_before();
-  Walk walk = walk_begin<C::kThreads>(kv_len, n_kv, T, batch, Hkv * np,
-                                      *reinterpret_cast<WalkShared<C::kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
+  Walk walk = walk_begin<kThreads>(kv_len, n_kv, T, batch, Hkv * np,
+                                      *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == C::kWarpK || warp == C::kWarpV) {
+  if (warp == kWarpK || warp == kWarpV) {
     // ---------------- TMA producers ----------------
     if (lane == 0) {
-      const bool is_k = warp == C::kWarpK;
+      const bool is_k = warp == kWarpK;
       const CUtensorMap* map = is_k ? &map_k : &map_v;
       const int full = is_k ? C::B_KFULL : C::B_VFULL, empty = is_k ? C::B_KEMPTY : C::B_VEMPTY;
       const int NS = is_k ? C::KS : C::VS;
       const uint32_t base = sb + (uint32_t)(is_k ? C::K_OFF : C::V_OFF);
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+      // K and V pass through the L2 once, unless several row-tile pairs read them
+      const uint64_t policy = np > 1 ? l2_evict_normal() : l2_evict_first();
       int slot = 0, issued = 0;
       uint32_t phase = 1;  // parity of the slot's last release
-      bool ok = true;
+      // The query rows go first: behind the first tiles of every SM they would wait for all of those.
+      bool ok = walk.u >= walk.u1 || mbar_wait_or_abort(bar(C::B_GO), 0, abort_flag);
       while (ok && walk.next()) {
         const int g = walk.item / np;
         for (int x = 0; x < walk.n; ++x) {
@@ -153,7 +175,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           mbar_expect_tx(bar(full + slot), C::kTile);
 #pragma unroll
           for (int h2 = 0; h2 < D / 64; ++h2)
-            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, g, (walk.j0 + x) * kRows, walk.s, bar(full + slot));
+            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, g, (walk.j0 + x) * kRows, walk.s, bar(full + slot), policy);
           ++issued;
           if (++slot == NS) {
             slot = 0;
@@ -164,123 +186,132 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // The copies in flight land before the CTA may exit.
       for (int x = max(0, issued - NS); x < issued; ++x) mbar_wait(bar(full + x % NS), (uint32_t)(x / NS) & 1u);
     }
-  } else if (warp == C::kWarpMMA) {
+  } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q and K both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // weights (tensor memory), V MN-major
+      constexpr int kParts = LO ? 2 : 1;                        // of a weight: high and low
       bool ok = true;
       int kit = 0, vit = 0, seg = 0;  // K and V tiles taken so far, segments
-      int cnt = 0;                    // key tiles multiplied so far (by each row tile that has rows)
-      int cnt1 = 0;                   // the same of row tile B
-      auto scores_of = [&](int t, int buf) {  // scores of row tile t and the K tile kit -> buffer buf
-        const uint32_t kt = sb + (uint32_t)(C::K_OFF + (kit % C::KS) * C::kTile);
-        const uint32_t qb = sb + (uint32_t)(t * C::kTile);
-#pragma unroll
-        for (int h2 = 0; h2 < D / 64; ++h2)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + 128u * (uint32_t)buf, desc_kmajor_sw128(qb + h2 * kHalf + kk * 32),
-                      desc_kmajor_sw128(kt + h2 * kHalf + kk * 32), kIdS, (h2 | kk) ? 1u : 0u);
-        umma_commit(bar(C::B_SFULL + buf));
-      };
+      int cnt[2] = {0, 0};            // products with the weights of each group
       auto wait_k = [&]() {
         const bool r = mbar_wait_or_abort(bar(C::B_KFULL + kit % C::KS), (uint32_t)(kit / C::KS) & 1u, abort_flag);
         tc_fence_after();
         return r;
       };
+      auto scores_of = [&](int t) {  // group t's scores with the K tile kit
+        const uint32_t kt = sb + (uint32_t)(C::K_OFF + (kit % C::KS) * C::kTile);
+        const uint32_t qb = sb + (uint32_t)(NT == 2 ? t * C::kTile : 0);
+#pragma unroll
+        for (int h2 = 0; h2 < D / 64; ++h2)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem + 128u * (uint32_t)t, desc_kmajor_sw128(qb + h2 * kHalf + kk * 32),
+                      desc_kmajor_sw128(kt + h2 * kHalf + kk * 32), kIdS, (h2 | kk) ? 1u : 0u);
+        umma_commit(bar(C::B_SFULL + t));
+      };
       auto free_k = [&]() {
         umma_commit(bar(C::B_KEMPTY + kit % C::KS));
         ++kit;
       };
-      auto output_of = [&](int t, int buf, bool first) {  // O_t += weights of buffer buf x V tile vit
+      auto output_of = [&](int t, bool first) {  // O_t += group t's weights x the V tile vit
         const uint32_t vt = sb + (uint32_t)(C::V_OFF + (vit % C::VS) * C::kTile);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)  // the weights' high and low parts
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
           for (int kk = 0; kk < kRows / 16; ++kk)
-            umma_bf16_ta(tmem + C::col_o(t), tmem + 128u * (uint32_t)buf + (uint32_t)(64 * part + 8 * kk),
+            umma_bf16_ta(tmem + col_o(t), tmem + 128u * (uint32_t)t + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1) + 16 * part),
                          desc_mnmajor_sw128(vt + kk * 2048, kHalf), kIdO, (!first || part || kk) ? 1u : 0u);
         umma_commit(bar(C::B_PFREE + t));
+        ++cnt[t];
+      };
+      auto wait_weights = [&](int t) {
+        const bool r = mbar_wait_or_abort(bar(C::B_PREADY + t), (uint32_t)cnt[t] & 1u, abort_flag);
+        tc_fence_after();
+        return r;
+      };
+      auto wait_v = [&]() {
+        return mbar_wait_or_abort(bar(C::B_VFULL + vit % C::VS), (uint32_t)(vit / C::VS) & 1u, abort_flag);
+      };
+      auto free_v = [&]() {
+        umma_commit(bar(C::B_VEMPTY + vit % C::VS));
+        ++vit;
       };
       while (ok && walk.next()) {
         const int n = walk.n;
+        ok = mbar_wait_or_abort(bar(C::B_QFULL), (uint32_t)seg & 1u, abort_flag) && wait_k();
+        ++seg;
+        if (!ok) break;
         if constexpr (NT == 1) {
-          ok = mbar_wait_or_abort(bar(C::B_QFULL), (uint32_t)seg & 1u, abort_flag) && wait_k();
-          if (!ok) break;
-          tc_fence_after();
-          scores_of(0, cnt & 1);
+          // key tile x belongs to group x & 1
+          scores_of(0);
           free_k();
-          for (int x = 0; ok && x < n; ++x, ++cnt) {
-            const int buf = cnt & 1;
-            if (x + 1 < n) {  // buffer buf ^ 1: its weights were multiplied with the V tile before
-              ok = wait_k();
-              if (!ok) break;
-              scores_of(0, buf ^ 1);
-              free_k();
-            }
-            ok = mbar_wait_or_abort(bar(C::B_VFULL + vit % C::VS), (uint32_t)(vit / C::VS) & 1u, abort_flag) &&
-                 mbar_wait_or_abort(bar(C::B_PREADY + buf), (uint32_t)(cnt >> 1) & 1u, abort_flag);
+          if (n > 1) {
+            ok = wait_k();
             if (!ok) break;
-            tc_fence_after();
-            output_of(0, buf, x == 0);
-            umma_commit(bar(C::B_VEMPTY + vit % C::VS));
-            ++vit;
+            scores_of(1);
+            free_k();
           }
+          for (int x = 0; ok && x < n; x += 2)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || x + t >= n) continue;
+              ok = wait_v() && wait_weights(t);
+              if (!ok) continue;
+              output_of(t, x == 0);
+              free_v();
+              if (x + t + 2 < n) {
+                ok = wait_k();
+                if (!ok) continue;
+                scores_of(t);
+                free_k();
+              }
+            }
         } else {
           const int pair = walk.item % np;
           const bool two = R - pair * 256 > kRows;
-          ok = mbar_wait_or_abort(bar(C::B_QFULL), (uint32_t)seg & 1u, abort_flag) &&
-               mbar_wait_or_abort(bar(C::B_QFULL + NT - 1), (uint32_t)seg & 1u, abort_flag) && wait_k();
-          if (!ok) break;
-          tc_fence_after();
-          scores_of(0, 0);
-          if (two) scores_of(1, 1);
+          scores_of(0);
+          if (two) scores_of(1);
           free_k();
           for (int x = 0; ok && x < n; ++x) {
-            ok = mbar_wait_or_abort(bar(C::B_VFULL + vit % C::VS), (uint32_t)(vit / C::VS) & 1u, abort_flag) &&
-                 mbar_wait_or_abort(bar(C::B_PREADY), (uint32_t)cnt & 1u, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            output_of(0, 0, x == 0);
-            ++cnt;
             const bool more = x + 1 < n;
+            ok = wait_v() && wait_weights(0);
+            if (!ok) break;
+            output_of(0, x == 0);
             if (more) {
               ok = wait_k();
               if (!ok) break;
-              scores_of(0, 0);
+              scores_of(0);
             }
             if (two) {
-              ok = mbar_wait_or_abort(bar(C::B_PREADY + 1), (uint32_t)cnt1 & 1u, abort_flag);
+              ok = wait_weights(1);
               if (!ok) break;
-              tc_fence_after();
-              output_of(NT - 1, 1, x == 0);
-              ++cnt1;
-              if (more) scores_of(1, 1);
+              output_of(1, x == 0);
+              if (more) scores_of(1);
             }
-            umma_commit(bar(C::B_VEMPTY + vit % C::VS));
-            ++vit;
+            free_v();
             if (more) free_k();
           }
         }
-        ++seg;
       }
       if (!ok) fail();
       umma_commit(bar(C::B_DRAIN));
       mbar_wait(bar(C::B_DRAIN), 0);
     }
   } else {
-    // ---------------- softmax and output: warps 4 t .. 4 t + 3 row tile t, thread = query row ----------------
+    // ---------------- softmax and output: group t = warps 4 t .. 4 t + 3, thread = query row ----------------
     const int t = warp >> 2;
     const int r = tid & (kRows - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t to = tmem + lanes + C::col_o(t);
+    const uint32_t ts = tmem + lanes + 128u * (uint32_t)t;
     const float lim = 8.f / qscale;
     const float2 qs2 = {qscale, qscale};
+    float2* join = reinterpret_cast<float2*>(smem + C::JOIN_OFF);
     bool ok = true;
-    int cnt = 0, seg = 0;
+    int cnt = 0, seg = 0;  // key tiles of this group so far, segments
+    int vit = 0;           // V tiles of the segments before
     uint32_t sync_phase = 0;
-    int vit = 0;  // V tiles so far
     auto sync = [&]() {
       mbar_arrive(bar(C::B_SYNC));
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SYNC), sync_phase, abort_flag)) && ok;
@@ -290,106 +321,116 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int64_t seq = walk.s;
       const int g = walk.item / np, pair = walk.item - g * np;
       const int L = (int)walk.L;
-      const int base = pair * (NT * kRows) + t * kRows;  // first query row of the tile
-      const int nr = min(kRows, R - base);                     // rows of the tile (none: below 1)
-      // Q rows of the tile; the last use of its buffer ended with the segment before
+      const int base = NT == 2 ? pair * 256 + t * kRows : 0;  // first query row of the group
+      const int nr = min(kRows, R - base);                     // its rows (none: below 1)
+      if (seg > 0) sync();  // the segment before is read out everywhere
+      if (!ok) break;
+      // Q rows, 16 bytes a copy, all in flight at once
       if (nr > 0) {
-        const int fill = (nr + 31) & ~31;  // the rows of warps that take part
-        constexpr int CH = D / 8;          // 16-byte chunks of a row
-        for (int e = r; e < fill * CH; e += kRows) {
-          const int row = e / CH, c = e % CH;
-          const bool held = row < nr;
-          const int i = (base + row) / G, hg = (base + row) - i * G;
-          cp_async16(smem + t * C::kTile + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+        constexpr int CH = D / 8;  // 16-byte chunks of a row; rows that hold no query are 0
+        for (int e = NT == 2 ? r : tid; e < kRows * CH; e += NT == 2 ? kRows : kSoftmax) {
+          const int row = e / CH, c = e % CH, qr = row % (kRows / REP);
+          const bool held = qr < nr;
+          const int i = (base + qr) / G, hg = (base + qr) - i * G;
+          cp_async16(smem + (NT == 2 ? t * C::kTile : 0) + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
                      held ? q + ((seq * T + i) * H + g * G + hg) * D + c * 8 : q, held);
         }
         cp_async_commit();
-        cp_async_wait<0>();
-        fence_async_smem();
       }
-      mbar_arrive(bar(C::B_QFULL + t));
-      sync();  // the segment before is read out everywhere
+      if (seg == 0) mbar_arrive(bar(C::B_GO));
+      cp_async_wait<0>();
+      fence_async_smem();
+      mbar_arrive(bar(C::B_QFULL));
       if (tid < kDraftWords) odd_rows[((seg + 1) & 1) * kDraftWords + tid] = 0u;
       uint32_t* odd = odd_rows + (seg & 1) * kDraftWords;
-      if (parent) {
-        if (draft_tree_build<C::kSoftmax>(tree, parent + seq * T, T, tid, sync) && status)
+      const bool treed = parent && (walk.j0 + walk.n) * kRows > L;  // the segment reaches behind the context
+      if (treed) {
+        if (draft_tree_build<kSoftmax>(tree, parent + seq * T, T, tid, sync) && status)
           atomicOr(status, kStatusBadIndex);
       }
       if (!ok) break;
       ++seg;
-      if (nr <= 0) {  // this row tile has no rows here
-        vit += walk.n;
-        continue;
-      }
-      const int slot_i = min(base + r, R - 1) / G;  // drafted token of this row
-      const bool token = !parent || tree.up[slot_i] == kRoot;
-      const bool warp_rows = (warp & 3) * 32 < nr;  // the warp has rows
+      const int vit0 = vit;
+      vit += walk.n;
+      if (NT == 2 && nr <= 0) continue;  // this group has no rows here
+      // This thread's query row of the tile, and its share of the tile's columns: blocks [cb, cb + kBlocks)
+      // of 32.
+      constexpr int kBlocks = 4 / REP;
+      const int qr = r % (kRows / REP), cb = r / (kRows / REP) * kBlocks;
+      const int slot_i = min(base + qr, R - 1) / G;  // drafted token of this row
+      // an empty slot; where the segment ends within the context, the merge learns it from another part
+      const bool empty = treed && tree.end[slot_i] != kRoot;
+      const bool warp_rows = (qr & ~31) < nr;       // the warp has rows
       float m_run = -INFINITY;                      // running max of the row's scores
       float2 l2 = {0.f, 0.f};                       // sum of the row's weights, relative to m_run
-      for (int x = 0; x < walk.n; ++x, ++cnt, ++vit) {
-        const int buf = NT == 2 ? t : cnt & 1;
-        const uint32_t par = (uint32_t)(NT == 2 ? cnt : cnt >> 1) & 1u;
-        const uint32_t ts = tmem + lanes + 128u * (uint32_t)buf;
+      bool any = false;                             // the group had a key tile
+      const int ahead_at = max(0, (walk.n - 10) & ~1);
+      for (int x = NT == 2 ? 0 : t; x < walk.n; x += NT == 2 ? 1 : 2, ++cnt) {
         const int t0 = (walk.j0 + x) * kRows;
         const bool tail = t0 + kRows > L;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + buf), par, abort_flag));
+        if (t == 0 && x == ahead_at) {
+          // the next segment's query rows and tree are brought to the L2 meanwhile
+          Walk ahead = walk;
+          if (ahead.next()) {
+            const int g2 = ahead.item / np, base2 = NT == 2 ? (ahead.item - g2 * np) * 256 : 0;
+            for (int e = r; e < min(NT * kRows, R - base2) * (D / 64); e += kRows) {
+              const int rr = base2 + e / (D / 64), i = rr / G;
+              prefetch_l2(q + (((int64_t)ahead.s * T + i) * H + g2 * G + (rr - i * G)) * D + (e % (D / 64)) * 64);
+            }
+            if (parent && r * 32 < T) prefetch_l2(parent + (int64_t)ahead.s * T + r * 32);
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + t), (uint32_t)cnt & 1u, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        if (tail && t == 0) {
-          // V rows behind the context: thread = row of the V tile.  The scores are in, so the V tile two
-          // before has been multiplied and the wait below cannot take an earlier fill of the slot for this one.
-          const int vs = vit % C::VS;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)(vit / C::VS) & 1u, abort_flag));
-          if (!ok) break;
-          const int j = t0 + r - L;
-          if (j >= 0) {
-            uint8_t* row = smem + C::V_OFF + vs * C::kTile + r * 128;
-            const bool held = j < T && (!parent || tree.up[j] == kRoot);
-            bool any = false;
-#pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* p = reinterpret_cast<uint4*>(row + (c >> 3) * kHalf + (c & 7) * 16);
-              uint4 w = *p;
-              uint32_t* a = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((a[e] & 0x7F80u) == 0x7F80u) {
-                  a[e] &= 0xFFFF0000u;
-                  any = true;
-                }
-                if ((a[e] & 0x7F800000u) == 0x7F800000u) {
-                  a[e] &= 0xFFFFu;
-                  any = true;
-                }
-                if (!held) a[e] = 0u;
-              }
-              if (any || !held) *p = w;
-            }
-            if (held && any) atomicOr(&odd[j >> 5], 1u << (j & 31));
-          }
-          fence_async_smem();
-        }
         if (warp_rows) {
-          uint32_t raw[4][32];
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) tmem_ld32_issue(ts + (uint32_t)(32 * c4), raw[c4]);
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) tmem_wait_ld(raw[c4]);
-          if (tail) {
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-              const int off = t0 + 32 * c4 - L;
-              const uint32_t w = parent ? mask_word(tree.anc[slot_i], off) : chain_word(slot_i, off);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) raw[c4][c] = ((w >> c) & 1u) ? raw[c4][c] : 0xFF800000u;  // -inf
-            }
-          }
+          // 32 columns at a time, the next load in flight: first the row's max, then, from the two blocks
+          // that are still in registers on, the weights
+          uint32_t xa[32], xb[32];
+          auto issue = [&](int c4, uint32_t(&x)[32]) { tmem_ld32_issue(ts + (uint32_t)(32 * c4), x); };
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto mask = [&](int c4, uint32_t(&x)[32]) {
+            if (!tail) return;
+            const int off = t0 + 32 * c4 - L;
+            const uint32_t w = parent ? mask_word(tree.anc[slot_i], off) : chain_word(slot_i, off);
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4)
+            for (int c = 0; c < 32; ++c) x[c] = ((w >> c) & 1u) ? x[c] : 0xFF800000u;  // -inf
+          };
+          auto look = [&](int c4, uint32_t(&x)[32]) {
+            mask(c4, x);
+            if (NT == 1 && scores && qr < nr) {
+              float* out = scores + ((seq * Hkv + g) * R + qr) * score_stride + t0 + 32 * c4;
+#pragma unroll
+              for (int c = 0; c < 32; c += 4)
+                *reinterpret_cast<float4*>(out + c) =
+                    make_float4(__uint_as_float(x[c]) * qscale, __uint_as_float(x[c + 1]) * qscale,
+                                __uint_as_float(x[c + 2]) * qscale, __uint_as_float(x[c + 3]) * qscale);
+            }
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < 32; c += 2)
-              m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(raw[c4][c]), __uint_as_float(raw[c4][c + 1]));
+              m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          };
+          issue(cb, xa);
+          tmem_wait_ld(xa);
+          if constexpr (kBlocks == 1) {
+            look(cb, xa);
+          } else {
+            issue(cb + 1, xb);
+            look(cb, xa);
+            tmem_wait_ld(xb);
+            if constexpr (kBlocks == 4) {
+              issue(2, xa);
+              look(1, xb);
+              tmem_wait_ld(xa);
+              issue(3, xb);
+              look(2, xa);
+              tmem_wait_ld(xb);
+              look(3, xb);
+            } else {
+              look(cb + 1, xb);
+            }
+          }
           const float tmax = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           // the max moves only when a weight would exceed 2^8
           const bool raise = tmax > m_run + lim;  // also the first visible key of the row (m_run = -inf)
@@ -406,25 +447,46 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           }
           const float nmq = m_run == -INFINITY ? 0.f : -m_run * qscale;
           const float2 nmq2 = {nmq, nmq};
-          // the weights over the scores: pairs (2 i, 2 i + 1), high parts in columns 0-63, low parts in 64-127
+          // the weights of a block over its scores: pairs (2 i, 2 i + 1), high parts in the block's columns
+          // 0-15, low parts in its columns 16-31
           float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
+          auto weigh = [&](int c4, const uint32_t(&x)[32]) {
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 e = ffma2(make_float2(__uint_as_float(raw[c4][2 * i]), __uint_as_float(raw[c4][2 * i + 1])),
-                                     qs2, nmq2);
+              const float2 e = ffma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), qs2, nmq2);
               const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));  // 0 where masked
               ls[i & 1] = fadd2(ls[i & 1], p);
               hi[i] = pack_bf16(p.x, p.y);
-              lo[i] = pack_bf16(p.x - bf16_lo(hi[i]), p.y - bf16_hi(hi[i]));
+              if (LO) lo[i] = pack_bf16(p.x - bf16_lo(hi[i]), p.y - bf16_hi(hi[i]));
             }
-            tmem_st16_issue(ts + (uint32_t)(16 * c4), hi);
-            tmem_st16_issue(ts + (uint32_t)(64 + 16 * c4), lo);
+            tmem_st16_issue(ts + (uint32_t)(32 * c4), hi);
+            if (LO) tmem_st16_issue(ts + (uint32_t)(32 * c4 + 16), lo);
+          };
+          if constexpr (kBlocks == 1) {
+            weigh(cb, xa);
+          } else if constexpr (kBlocks == 2) {
+            weigh(cb, xa);
+            weigh(cb + 1, xb);
+          } else {
+            weigh(2, xa);
+            issue(0, xa);
+            weigh(3, xb);
+            tmem_wait_ld(xa);
+            issue(1, xb);
+            mask(0, xa);
+            weigh(0, xa);
+            tmem_wait_ld(xb);
+            mask(1, xb);
+            weigh(1, xb);
+          }
+          if constexpr (REP > 1) {  // the other copies' columns count nothing here
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4)
+              if (c4 / kBlocks != cb / kBlocks) tmem_zero32_issue(ts + (uint32_t)(32 * c4));
           }
           l2 = fadd2(l2, fadd2(ls[0], ls[1]));
-          if (__any_sync(0xFFFFFFFFu, resc)) {  // O holds earlier tiles (x > 0): rescale it once they are in
+          if (__any_sync(0xFFFFFFFFu, resc)) {  // the group's output holds earlier tiles: rescale it once they are in
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag))) {
               ok = false;
               break;
@@ -433,90 +495,196 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t ov[16];
-              tmem_ld<16>(to + c, ov);
+              tmem_ld<16>(tmem + lanes + col_o(t) + c, ov);
 #pragma unroll
               for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-              tmem_st16_issue(to + c, ov);
+              tmem_st16_issue(tmem + lanes + col_o(t) + c, ov);
             }
           }
           tmem_wait_st();
         }
-        // Two score buffers: these scores say only that the product before the last one is in.  The wait
-        // behind the segment's last tile can tell its product from that of the tile before alone, so
-        // that one is waited for here.
-        if (NT == 1 && x + 1 == walk.n && cnt > 0) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag));
+        if (tail && (NT == 1 || t == 0)) {
+          // V rows behind the context.  The scores are in, and with them this
+          // group's product before, so the wait cannot take an earlier fill of the V slot for this one.
+          const int vs = (vit0 + x) % C::VS;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)((vit0 + x) / C::VS) & 1u, abort_flag));
           if (!ok) break;
+          uint8_t* vt = smem + C::V_OFF + vs * C::kTile;
+          constexpr int CH = D / 8;
+          for (int e = max(0, L - t0) * CH + r; e < kRows * CH; e += kRows) {  // 16 bytes each, CH to a row
+            const int row = e / CH, c = e % CH, j = t0 + row - L;
+            const bool held = j < T && (!parent || tree.end[j] == kRoot);
+            uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + row * 128 + (c & 7) * 16);
+            if (!held) {
+              *p = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 w = *p;
+            uint32_t* a = reinterpret_cast<uint32_t*>(&w);
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((a[i] & 0x7F80u) == 0x7F80u) {
+                a[i] &= 0xFFFF0000u;
+                found = true;
+              }
+              if ((a[i] & 0x7F800000u) == 0x7F800000u) {
+                a[i] &= 0xFFFFu;
+                found = true;
+              }
+            }
+            if (found) {
+              *p = w;
+              atomicOr(&odd[j >> 5], 1u << (j & 31));
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
         }
         tc_fence_before();
-        mbar_arrive(bar(C::B_PREADY + buf));
+        mbar_arrive(bar(C::B_PREADY + t));
+        any = true;
       }
       if (!ok) break;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      if (!warp_rows) continue;
+      if (any) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+      }
       float l = l2.x + l2.y;
-      if (!token) {
+      float m = m_run == -INFINITY ? -INFINITY : m_run * qscale;  // log2 domain
+      // What this lane's two outputs count: w0 O_0 + w1 O_1; one row tile: both groups' key tiles and all
+      // copies of the row joined, each group taking half of the columns.
+      int c0 = 0, c1 = D;
+      float w0 = t == 0 ? 1.f : 0.f, w1 = t == 1 ? 1.f : 0.f;
+      bool use0 = t == 0, use1 = t == 1;
+      if constexpr (NT == 1) {
+        join[t * kRows + r] = make_float2(m, l);
+        tc_fence_before();
+        sync();
+        if (!ok) break;
+        tc_fence_after();
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2 * REP; ++x) top = fmaxf(top, join[x * (kRows / REP) + qr].x);
+#pragma unroll
+        for (int x = 0; x < 2 * REP; ++x) {
+          const float2 a = join[x * (kRows / REP) + qr];
+          const float w = a.y == 0.f ? 0.f : a.x == -INFINITY ? 1.f : exp2f(a.x - top);
+          sum += w == 0.f ? 0.f : w * a.y;
+          if (x == r / (kRows / REP)) w0 = w;
+          if (x == REP + r / (kRows / REP)) w1 = w;
+        }
+        m = top;
+        l = sum;
+        use0 = true;
+        use1 = walk.n > 1;
+        c0 = t * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      if (empty) {
         l = 0.f;
-        m_run = -INFINITY;
+        m = INFINITY;
       }
       const bool whole = walk.whole();
-      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int64_t row = (seq * T + slot_i) * H + g * G + (base + r - slot_i * G);
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + walk.slot()) * (NT * kRows) + t * kRows + r;
+      const int64_t part = (int64_t)blockIdx.x * 2 + walk.slot();
       const uint32_t any_odd = odd[0] | odd[1] | odd[2] | odd[3] | odd[4] | odd[5] | odd[6] | odd[7];
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t ov[32];
-        __syncwarp();  // the load below takes the whole warp
-        tmem_ld32_issue(to + c0, ov);
-        tmem_wait_ld(ov);
-        if (r >= nr) continue;
-        if (l == 0.f) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = 0u;
-        }
-        if (any_odd && token) {
+      // Four columns of a row of this item: its slot, its sum.
+      auto put = [&](int row, int c, float4 x, float sum) {
+        const int i = (base + row) / G;
+        if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (any_odd && !(treed && tree.end[i] != kRoot)) {
           // values that are not finite, of the rows this token sees in this segment
-#pragma unroll 1
           for (int j = 0; j < T; ++j) {
             if (!((odd[j >> 5] >> (j & 31)) & 1u)) continue;
-            if (parent ? !((tree.anc[slot_i][j >> 5] >> (j & 31)) & 1u) : j > slot_i) continue;
-            const uint32_t* vr = reinterpret_cast<const uint32_t*>(v + (((seq * n_kv + L + j) * Hkv) + g) * D + c0);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t w = vr[i];
-              if ((w & 0x7F80u) == 0x7F80u) ov[2 * i] = __float_as_uint(__uint_as_float(ov[2 * i]) + bf16_lo(w));
-              if ((w & 0x7F800000u) == 0x7F800000u)
-                ov[2 * i + 1] = __float_as_uint(__uint_as_float(ov[2 * i + 1]) + bf16_hi(w));
-            }
+            if (parent ? !((tree.anc[i][j >> 5] >> (j & 31)) & 1u) : j > i) continue;
+            const uint2 y = *reinterpret_cast<const uint2*>(v + ((seq * n_kv + L + j) * Hkv + g) * D + c);
+            if ((y.x & 0x7F80u) == 0x7F80u) x.x += bf16_lo(y.x);
+            if ((y.x & 0x7F800000u) == 0x7F800000u) x.y += bf16_hi(y.x);
+            if ((y.y & 0x7F80u) == 0x7F80u) x.z += bf16_lo(y.y);
+            if ((y.y & 0x7F800000u) == 0x7F800000u) x.w += bf16_hi(y.y);
           }
         }
         if (whole) {
-          uint16_t* orow = o + row * D + c0;
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint4 w;
-            w.x = pack_bf16(__uint_as_float(ov[8 * q4 + 0]) * inv, __uint_as_float(ov[8 * q4 + 1]) * inv);
-            w.y = pack_bf16(__uint_as_float(ov[8 * q4 + 2]) * inv, __uint_as_float(ov[8 * q4 + 3]) * inv);
-            w.z = pack_bf16(__uint_as_float(ov[8 * q4 + 4]) * inv, __uint_as_float(ov[8 * q4 + 5]) * inv);
-            w.w = pack_bf16(__uint_as_float(ov[8 * q4 + 6]) * inv, __uint_as_float(ov[8 * q4 + 7]) * inv);
-            *reinterpret_cast<uint4*>(orow + 8 * q4) = w;
-          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int64_t at = (seq * T + i) * H + g * G + (base + row - i * G);
+          *reinterpret_cast<uint2*>(o + at * D + c) =
+              make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
         } else {
-          float* prt = work.part_o + prow * D + c0;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(prt + i) = make_uint4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+          work.part_o[(part * (D / 4) + c / 4) * (NT * kRows) + (NT == 2 ? t * kRows : 0) + row] = x;
         }
+      };
+      auto read16 = [&](int c, float(&ov)[16]) {  // 16 columns of this lane's share; the whole warp calls
+        uint32_t x0[16], x1[16];
+        __syncwarp();
+        if (use0) tmem_ld<16>(tmem + lanes + col_o(0) + c, x0);
+        if (use1) tmem_ld<16>(tmem + lanes + col_o(1) + c, x1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          // an output that saw nothing is left out: it may hold 0 x inf
+          ov[i] = use0 && w0 != 0.f ? w0 * __uint_as_float(x0[i]) : 0.f;
+          if (use1 && w1 != 0.f) ov[i] = fmaf(w1, __uint_as_float(x1[i]), ov[i]);
+        }
+      };
+      if constexpr (REP == 1) {
+        if (warp_rows) {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 16) {
+            float ov[16];
+            read16(c, ov);
+            if (qr < nr) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) put(qr, c + i, make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]), l);
+            }
+          }
+        }
+      } else {
+        // The copies' shares are added through shared memory (the query rows' place, all scores are
+        // formed): kCols columns of each half a round.
+        constexpr int kCols = D / 4, kRowsOf = kRows / REP;
+        float4* buf = reinterpret_cast<float4*>(smem);  // [warp][kCols / 4][32]
+        float* sums = reinterpret_cast<float*>(join);   // the rows' sums, once everyone has read the parts
+        sync();
+        if (!ok) break;
+        if (t == 0 && r < kRowsOf) sums[r] = l;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += kCols) {
+          if (warp_rows) {
+#pragma unroll 1
+            for (int x = 0; x < kCols; x += 16) {
+              float ov[16];
+              read16(c0 + c + x, ov);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                buf[(warp * (kCols / 4) + (x + i) / 4) * 32 + lane] = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+            }
+          }
+          sync();
+          if (!ok) break;
+          for (int e = tid; e < kRowsOf * 2 * (kCols / 4); e += kSoftmax) {
+            const int row = e % kRowsOf, c4 = e / kRowsOf % (kCols / 4), half = e / kRowsOf / (kCols / 4);
+            if (row >= nr) continue;
+            float4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int y = 0; y < REP; ++y) {
+              const int lanes_of = half * kRows + y * kRowsOf + row;  // lane of the row's copy y in that group
+              const float4 z = buf[(lanes_of / 32 * (kCols / 4) + c4) * 32 + lanes_of % 32];
+              x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
+            }
+            put(row, half * (D / 2) + c + 4 * c4, x, sums[row]);
+          }
+          sync();
+          if (!ok) break;
+        }
+        if (!ok) break;
       }
       __syncwarp();
-      if (r < nr) {
+      if (qr < nr && r == qr && (NT == 2 || t == 0)) {
         if (!whole)
-          work.part_ml[prow] = make_float2(m_run == -INFINITY ? -INFINITY : m_run * qscale, l);
+          work.part_ml[part * (NT * kRows) + (NT == 2 ? t * kRows : 0) + qr] = make_float2(m, l);
         else if (lse)
-          lse[row] = l == 0.f ? -INFINITY : (m_run * qscale + log2f(l)) * kLn2;
+          lse[(seq * T + slot_i) * H + g * G + (base + qr - slot_i * G)] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
     }
     if (!ok && lane == 0) fail();
@@ -524,111 +692,164 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kWarpMMA) {
+  if (warp == kWarpMMA) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
 }
 
 // Rows whose item several CTAs hold: the parts joined; rows of sequences whose length is out of
-// range: 0 and -inf.  SPLIT = false: a warp per row takes the parts one after another (items on few
-// CTAs each); true: a CTA per row, its warps share the parts (few items, each on many CTAs).
-constexpr int kMergeThreads = 256;
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kMergeThreads)
-    tree_attn_merge_kernel(Work work, uint16_t* __restrict__ o,
-                           float* __restrict__ lse, int batch, int T, int H, int Hkv, int tile_rows, int grid) {
-  constexpr int NW = kMergeThreads / 32, LN = D / 4, PER = 32 / LN;  // lanes of a row, parts a warp takes at once
-  __shared__ float sm_l[NW], sm_m[NW];
-  __shared__ float4 sm_o[NW][32];
+// range: 0 and -inf.  A CTA takes up to 32 rows of an item: lane = row, and where the item has fewer
+// rows the lanes share its parts; a warp takes 16 columns, and kSplits sets of warps share the parts.
+constexpr int kSplits = 4;
+struct MergeState {
+  float m, l;
+  float o[16];
+  bool empty;
+  __device__ void add(float m2, float l2, const float* o2) {
+    if (l2 == 0.f) return;
+    const float top = fmaxf(m, m2);
+    const float a = l == 0.f ? 0.f : m == -INFINITY ? 1.f : exp2f(m - top), b = m2 == -INFINITY ? 1.f : exp2f(m2 - top);
+    m = top;
+    l = a * l + b * l2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = (a == 0.f ? 0.f : a * o[i]) + b * o2[i];
+  }
+};
+template <int D>
+__global__ void __launch_bounds__(32 * (D / 16) * kSplits)
+    tree_attn_merge_kernel(Work work, uint16_t* __restrict__ o, float* __restrict__ lse, int batch, int T, int H,
+                           int Hkv, int tile_rows, int row_lanes, int grid) {
+  constexpr int CW = D / 16;  // warps side by side
+  __shared__ float sm_ml[kSplits / 2][CW][32][2];
+  __shared__ float4 sm_o[kSplits / 2][CW][4][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cw = warp % CW, split = warp / CW;
   const int64_t seq = blockIdx.y;
-  const int idx = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * NW + warp;  // i * H + h
-  if (idx >= T * H) return;
-  const int i = idx / H, h = idx - i * H, G = H / Hkv, g = h / G;
-  const int rr = i * G + (h - g * G), pair = rr / tile_rows, R = T * G, np = (R + tile_rows - 1) / tile_rows;
+  const int G = H / Hkv, R = T * G, np = (R + tile_rows - 1) / tile_rows, blocks = (R + row_lanes - 1) / row_lanes;
+  const int g = blockIdx.x / blocks, r = (blockIdx.x - g * blocks) * row_lanes + lane % row_lanes;  // query row
+  const int pair = (blockIdx.x - g * blocks) * row_lanes / tile_rows;  // row_lanes divides tile_rows
   const int64_t P = work.prefix[seq], tiles = work.prefix[seq + 1] - P, total = work.prefix[batch];
-  const int64_t row = seq * T * H + idx;
-  const int c = lane % LN, sub = lane / LN;
-  if (tiles == 0) {
-    if (SPLIT && warp != 0) return;
-    if (sub == 0) *reinterpret_cast<uint2*>(o + row * D + 4 * c) = make_uint2(0u, 0u);
-    if (lane == 0 && lse) lse[row] = -INFINITY;
-    return;
-  }
-  const int64_t units = total * Hkv * np, ctas = range_ctas(units, grid);
-  const int64_t u0 = P * Hkv * np + ((int64_t)g * np + pair) * tiles;
-  const int64_t c0 = range_of(u0, units, ctas), c1 = range_of(u0 + tiles - 1, units, ctas);
-  if (c0 == c1) return;
-  const int n = (int)(c1 - c0) + 1;
-  const int first_slot = range_begin(c0, units, ctas) == u0 ? 0 : 1;
-  auto part_row = [&](int p) {
-    return ((c0 + p) * 2 + (p == 0 ? first_slot : 0)) * (int64_t)tile_rows + (rr - pair * tile_rows);
-  };
-  const int p0 = SPLIT ? warp : 0, step = SPLIT ? NW : 1;
-  // max and sum over the warp's parts, then over the warps'
-  float m = -INFINITY, l = 0.f;
-  for (int p = p0 + step * lane; p < n; p += step * 32) {
-    const float2 ml = work.part_ml[part_row(p)];
-    const float mn = fmaxf(m, ml.x);
-    l = l * (m == -INFINITY ? 0.f : exp2f(m - mn)) + ml.y * (ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - mn));
-    m = mn;
-  }
-  const float M = warp_max(m);
-  l = warp_sum(l * (m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M)));
-  float4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int p = p0 + step * sub; p < n; p += step * PER) {
-    const int64_t pr = part_row(p);
-    const float2 ml = work.part_ml[pr];
-    const float4 x = *reinterpret_cast<const float4*>(work.part_o + pr * D + 4 * c);
-    if (ml.y == 0.f) continue;  // nothing visible there
-    const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
-    acc.x += w * x.x;
-    acc.y += w * x.y;
-    acc.z += w * x.z;
-    acc.w += w * x.w;
-  }
-  if constexpr (PER == 2) {
-    acc.x += __shfl_xor_sync(0xFFFFFFFFu, acc.x, 16);
-    acc.y += __shfl_xor_sync(0xFFFFFFFFu, acc.y, 16);
-    acc.z += __shfl_xor_sync(0xFFFFFFFFu, acc.z, 16);
-    acc.w += __shfl_xor_sync(0xFFFFFFFFu, acc.w, 16);
-  }
-  float top = M;
-  if constexpr (SPLIT) {
-    if (lane == 0) {
-      sm_m[warp] = M;
-      sm_l[warp] = l;
+  const int i = r / G;
+  const int64_t row = (seq * T + i) * H + g * G + (r - i * G);
+  const bool mine = r < R && lane < row_lanes && split == 0;  // writes the row
+  MergeState st;
+  st.m = -INFINITY;
+  st.l = 0.f;
+  st.empty = false;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) st.o[x] = 0.f;
+  if (tiles > 0) {
+    const int64_t units = total * Hkv * np, ctas = range_ctas(units, grid);
+    const int64_t u0 = P * Hkv * np + ((int64_t)g * np + pair) * tiles;
+    const int64_t first = range_of(u0, units, ctas), last = range_of(u0 + tiles - 1, units, ctas);
+    if (first == last) return;  // written by that CTA
+    const int n = (int)(last - first) + 1;
+    const int first_slot = range_begin(first, units, ctas) == u0 ? 0 : 1;
+    const int groups = 32 / row_lanes * kSplits, pr = min(r, R - 1) - pair * tile_rows;
+#pragma unroll 2
+    for (int p = split * (32 / row_lanes) + lane / row_lanes; p < n; p += groups) {
+      const int64_t part = (first + p) * 2 + (p == 0 ? first_slot : 0);
+      const float2 ml = work.part_ml[part * tile_rows + pr];
+      float4 x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = work.part_o[(part * (D / 4) + cw * 4 + c) * tile_rows + pr];
+      st.empty = st.empty || (ml.x == INFINITY && ml.y == 0.f);
+      st.add(ml.x, ml.y, reinterpret_cast<const float*>(x));
     }
-    sm_o[warp][lane] = acc;
+    // the lanes of a row, then the sets of warps
+    for (int off = row_lanes; off < 32; off *= 2) {
+      float o2[16];
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, st.m, off), l2 = __shfl_xor_sync(0xFFFFFFFFu, st.l, off);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o2[x] = __shfl_xor_sync(0xFFFFFFFFu, st.o[x], off);
+      const bool e2 = __shfl_xor_sync(0xFFFFFFFFu, (int)st.empty, off) != 0;
+      st.empty = st.empty || e2;
+      st.add(m2, l2, o2);
+    }
+#pragma unroll
+    for (int half = kSplits / 2; half >= 1; half /= 2) {
+      if (split >= half && split < 2 * half) {
+        sm_ml[split - half][cw][lane][0] = st.empty ? INFINITY : st.m;
+        sm_ml[split - half][cw][lane][1] = st.empty ? 0.f : st.l;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sm_o[split - half][cw][c][lane] = make_float4(st.o[4 * c], st.o[4 * c + 1], st.o[4 * c + 2], st.o[4 * c + 3]);
+      }
+      __syncthreads();
+      if (split < half) {
+        const float m2 = sm_ml[split][cw][lane][0], l2 = sm_ml[split][cw][lane][1];
+        float4 x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = sm_o[split][cw][c][lane];
+        st.empty = st.empty || (m2 == INFINITY && l2 == 0.f);
+        st.add(m2, l2, reinterpret_cast<const float*>(x));
+      }
+      __syncthreads();
+    }
+  }
+  if (!mine) return;
+  const bool none = st.empty || st.l == 0.f;
+  const float inv = none ? 0.f : 1.f / st.l;
+  uint32_t w[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) w[x] = none ? 0u : pack_bf16(st.o[2 * x] * inv, st.o[2 * x + 1] * inv);
+  uint4* out = reinterpret_cast<uint4*>(o + row * D + 16 * cw);
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (cw == 0 && lse) lse[row] = none ? -INFINITY : (st.m + log2f(st.l)) * kLn2;
+}
+
+// The weights the rows received, from the scores that the attention kept: thread = 4 rows of the
+// cache, the query rows added in order.
+constexpr int kWeighThreads = 128, kWeighRows = 512;
+__global__ void __launch_bounds__(kWeighThreads)
+    tree_attn_weigh_kernel(const float* __restrict__ scores, int64_t score_stride, const float* __restrict__ lse,
+                           const int32_t* __restrict__ kv_len, float* __restrict__ weight, int T, int64_t n_kv, int H,
+                           int Hkv) {
+  __shared__ float nlse2[kWeighRows];  // minus the LSE in the log2 domain; -inf: an empty slot
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t seq = blockIdx.y, L = context_len(kv_len, seq, T, n_kv);
+  const int64_t t = ((int64_t)blockIdx.x * kWeighThreads + threadIdx.x) * 4;
+  if (L < 0 || (int64_t)blockIdx.x * kWeighThreads * 4 >= L + T) return;
+  const int G = H / Hkv, R = T * G, rows = T * H;
+  float4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
+    const int n = min(kWeighRows, rows - r0);
     __syncthreads();
-    if (warp != 0) return;
-    top = -INFINITY;
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, sm_m[w]);
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < NW; ++w) {
-      if (sm_l[w] == 0.f) continue;
-      const float a = sm_m[w] == -INFINITY ? 1.f : exp2f(sm_m[w] - top);
-      const float4 x = sm_o[w][lane];
-      l += a * sm_l[w];
-      acc.x += a * x.x;
-      acc.y += a * x.y;
-      acc.z += a * x.z;
-      acc.w += a * x.w;
+    for (int x = threadIdx.x; x < n; x += kWeighThreads) {
+      const int g = (r0 + x) / R, r = r0 + x - g * R, i = r / G;
+      const float l = lse[(seq * T + i) * H + g * G + (r - i * G)];
+      nlse2[x] = l == -INFINITY ? -INFINITY : l * -kLog2e;
+    }
+    __syncthreads();
+    if (t >= L + T) continue;
+    const float* z = scores + (seq * rows + r0) * score_stride + t;
+#pragma unroll 8
+    for (int x = 0; x < n; ++x) {
+      const float nl = nlse2[x];
+      const float4 s = *reinterpret_cast<const float4*>(z + x * score_stride);
+      if (nl == -INFINITY) continue;
+      sum.x += fast_exp2(s.x + nl);
+      sum.y += fast_exp2(s.y + nl);
+      sum.z += fast_exp2(s.z + nl);
+      sum.w += fast_exp2(s.w + nl);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (sub == 0)
-    *reinterpret_cast<uint2*>(o + row * D + 4 * c) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lane == 0 && lse) lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+  float* w = weight + seq * n_kv + t;
+  if (t < L + T) w[0] = t < L ? w[0] + sum.x : sum.x;
+  if (t + 1 < L + T) w[1] = t + 1 < L ? w[1] + sum.y : sum.y;
+  if (t + 2 < L + T) w[2] = t + 2 < L ? w[2] + sum.z : sum.z;
+  if (t + 3 < L + T) w[3] = t + 3 < L ? w[3] + sum.w : sum.w;
 }
 
 int row_tiles(const Shape& s) { return s.n_q * (s.H / s.Hkv) > kRows ? 2 : 1; }
+
+// The weights come from kept scores while writing and reading those (8 bytes a query row and key) moves
+// less than reading K again (2 d bytes a KV head and key).
+bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) * 4 <= s.d; }
+int64_t score_stride(const Shape& s) { return (s.n_kv + kRows - 1) / kRows * kRows; }
 
 struct Layout {
   size_t prefix, part_o, part_ml, lse, weight, total;
@@ -643,36 +864,36 @@ Layout layout(const Shape& s, bool with_weight) {
   L.lse = L.part_ml + up(rows * sizeof(float2));
   L.weight = L.lse + (with_weight ? up((size_t)s.n_query * s.H * sizeof(float)) : 0);
   L.total = L.weight;
-  if (with_weight) L.total += up(cache_weight_workspace_bytes(s));
+  if (with_weight)
+    L.total += up(keeps_scores(s) ? (size_t)s.n_query * s.H * score_stride(s) * sizeof(float)
+                                  : cache_weight_workspace_bytes(s));
   return L;
 }
 
-template <int D, int NT>
+template <int D, int NT, int REP>
 cudaError_t launch(const Shape& s, const void* q, const void* k, const void* v, const int32_t* kv_len,
-                   const int32_t* parent, void* o, float* lse, Work work, int32_t* status, cudaStream_t st) {
+                   const int32_t* parent, void* o, float* lse, float* scores, int64_t score_stride, Work work,
+                   int32_t* status, cudaStream_t st) {
   using C = Cfg<D, NT>;
   CUtensorMap mk, mv;
   if (!map_cache_rows(&mk, k, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows) ||
       !map_cache_rows(&mv, v, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows))
     return cudaErrorNotSupported;
-  cudaError_t e = ensure_smem((const void*)tree_attn_kernel<D, NT>, C::kSmem);
+  cudaError_t e = ensure_smem((const void*)tree_attn_kernel<D, NT, REP>, C::kSmem);
   if (e != cudaSuccess) return e;
   const int R = (int)s.n_q * (s.H / s.Hkv), np = (R + NT * kRows - 1) / (NT * kRows);
   const int64_t items = (int64_t)s.batch * s.Hkv * np, most = items * ((s.n_kv + kRows - 1) / kRows);
   const int ctas = (int)(most < kMaxCtas ? most : kMaxCtas);
-  tree_attn_kernel<D, NT><<<ctas, C::kThreads, C::kSmem, st>>>(
-      mk, mv, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(v), kv_len, parent,
-      static_cast<uint16_t*>(o), lse, work, status, s.batch, (int)s.n_q, s.n_kv, s.H, s.Hkv,
-      s.scale * kLog2e);
-  e = cudaGetLastError();
+  e = launch_after(tree_attn_kernel<D, NT, REP>, dim3((unsigned)ctas), kThreads, st, C::kSmem, mk, mv,
+                   static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(v), kv_len, parent,
+                   static_cast<uint16_t*>(o), lse, scores, score_stride, work, status, s.batch, (int)s.n_q, s.n_kv, s.H,
+                   s.Hkv, s.scale * kLog2e);
   if (e != cudaSuccess) return e;
-  // a CTA per row where an item's parts are many, or where the rows are so few that one wave of CTAs
-  // takes them all
-  const bool split = items * 16 < ctas || (items * 4 < ctas && s.n_query * s.H <= 8 * kMaxCtas);
-  const int rows = (int)s.n_q * s.H, per = split ? 1 : kMergeThreads / 32;
-  return launch_after(split ? tree_attn_merge_kernel<D, true> : tree_attn_merge_kernel<D, false>,
-                      dim3((unsigned)((rows + per - 1) / per), (unsigned)s.batch), kMergeThreads, st, work,
-                      static_cast<uint16_t*>(o), lse, s.batch, (int)s.n_q, s.H, s.Hkv, NT * kRows, ctas);
+  int lanes = 1;  // lanes for rows
+  while (lanes < 32 && lanes < R) lanes *= 2;
+  return launch_after(tree_attn_merge_kernel<D>, dim3((unsigned)(s.Hkv * ((R + lanes - 1) / lanes)), (unsigned)s.batch),
+                      32 * (D / 16) * kSplits, st, 0, work, static_cast<uint16_t*>(o), lse, s.batch, (int)s.n_q, s.H, s.Hkv,
+                      NT * kRows, lanes, ctas);
 }
 
 }  // namespace
@@ -684,14 +905,23 @@ cudaError_t launch_tree_attn(const Shape& s, const void* q, const void* k, const
                              cudaStream_t st) {
   const Layout L = layout(s, weight != nullptr);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const Work work = {reinterpret_cast<int64_t*>(w + L.prefix), reinterpret_cast<float*>(w + L.part_o),
+  const Work work = {reinterpret_cast<int64_t*>(w + L.prefix), reinterpret_cast<float4*>(w + L.part_o),
                      reinterpret_cast<float2*>(w + L.part_ml)};
   if (weight && !lse) lse = reinterpret_cast<float*>(w + L.lse);
-  const auto run = s.d == 64 ? (row_tiles(s) == 1 ? launch<64, 1> : launch<64, 2>)
-                             : (row_tiles(s) == 1 ? launch<128, 1> : launch<128, 2>);
-  const cudaError_t e = run(s, q, k, v, kv_len, parent, o, lse, work, status, st);
+  const int64_t R = s.n_q * (s.H / s.Hkv);
+  const auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return R <= 32 ? launch<D, 1, 4> : R <= 64 ? launch<D, 1, 2> : R <= kRows ? launch<D, 1, 1> : launch<D, 2, 1>;
+  };
+  const auto run = s.d == 64 ? pick(std::integral_constant<int, 64>()) : pick(std::integral_constant<int, 128>());
+  const bool kept = weight && keeps_scores(s);
+  float* scores = kept ? reinterpret_cast<float*>(w + L.weight) : nullptr;
+  const cudaError_t e = run(s, q, k, v, kv_len, parent, o, lse, scores, score_stride(s), work, status, st);
   if (e != cudaSuccess || !weight) return e;
-  return launch_cache_weight(s, q, k, kv_len, parent, nullptr, lse, weight, nullptr, w + L.weight, st);
+  if (!kept) return launch_cache_weight(s, q, k, kv_len, parent, nullptr, lse, weight, nullptr, w + L.weight, st);
+  const int64_t per = 4 * kWeighThreads;
+  return launch_after(tree_attn_weigh_kernel, dim3((unsigned)((s.n_kv + per - 1) / per), (unsigned)s.batch),
+                      kWeighThreads, st, 0, scores, score_stride(s), lse, kv_len, weight, (int)s.n_q, s.n_kv, s.H, s.Hkv);
 }
 
 }  // namespace hisa

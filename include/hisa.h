@@ -347,7 +347,10 @@ hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_
  * head g = h / (H / Hk)), with z(t) = scale * q[s][i][h] . k[s][t][g],
  *   o[s][i][h]   = sum_{t in V(i)} softmax_t(z(t)) v[s][t][g]
  *   lse[s][i][h] = ln sum_{t in V(i)} exp(z(t))       (lse nullable)
- * An empty slot gives o = 0, lse = -inf.
+ * An empty slot gives o = 0, lse = -inf.  fp32 scores, sums and accumulation,
+ * bf16 output; with up to 64 query rows per KV head (T * H / Hk) the weights
+ * multiply V to 16 significant bits, with more as bf16 (each output then stays
+ * within 2^-8 sum_t softmax_t |v| of the exact one before its own rounding).
  * weight (nullable) [b][n_kv] fp32: the attention weight each row receives,
  *   a(t) = sum over slots i with t in V(i) and heads h of exp(z(t) - lse[s][i][h]),
  * is added on the context's rows (weight[s][t] += a(t), t < L) and replaces

@@ -4,7 +4,9 @@ Tolerances.  An fp32 score of d products is off by at most (d + 8) 2^-23 times s
 the tensor cores truncate), and its scaling, the exponential and the sums add a relative 2^-16; a weight that enters
 the product as a pair of bf16 numbers is off by 2^-16 more.  So a softmax weight is off by a relative
 delta = (d + 8) 2^-23 size + 2^-14 at most, numerator and denominator each, and
-    |o - ref|   <= 2^-8 |ref| + 2 delta sum p |v|      (2^-8: the output's rounding to bf16)
+    |o - ref|   <= 2^-8 |ref| + (2 delta + e) sum p |v|      (2^-8: the output's rounding to bf16)
+with e = 2^-8 where a KV head has more than 64 query rows (T H / Hk): there a weight enters the product as one bf16
+number, off by half a step of 8 significant bits, 2^-8 relative, in the numerator alone; else e = 0.
     |lse - ref| <= delta + 2^-22 |ref|
     |w - ref|   <= (delta + 2^-21 max |lse|) received + 2^-20 |ref| + 2^-110
 where 2^-110 covers fp32's range: a weight below 2^-126 has no relative precision and may count as 0, and at most
@@ -97,7 +99,8 @@ def check_tree(hs, x, H, Hk, d, weigh):
                                                         1 / math.sqrt(d))
     dl = delta(d, size)
     close(lse, rl, dl + 2.0**-22 * rl.abs().nan_to_num(0, 0, 0), "lse")
-    close(o, ro, 2.0**-8 * ro.abs() + 2 * dl * spread, "o")
+    e = 2.0**-8 if T * H // Hk > 64 else 0.0
+    close(o, ro, 2.0**-8 * ro.abs() + (2 * dl + e) * spread, "o")
     top = float(rl[rl > -math.inf].abs().max()) if (rl > -math.inf).any() else 0.0
     if weigh:
         want = ref.weight_after(x["weight"], received, x["kv_len"], T)
