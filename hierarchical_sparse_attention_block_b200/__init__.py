@@ -177,6 +177,18 @@ def _size(fn, p, two=False):
     return a.value
 
 
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
 def _workspace(nbytes, device):
     import torch
 
@@ -357,51 +369,49 @@ def _refuse(call, detail):
     raise HisaError(call, HISA_ERR_INVALID_ARG, detail)
 
 
-def _checked(call, device, **tensors):
-    """The addresses of name=(tensor, dtype, shape) in order.  The library takes dense tensors and trusts their
-    sizes, so each tensor has to be a contiguous CUDA tensor of that type and shape on `device` (None passes
-    through)."""
-    out = []
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            out.append(None)
-            continue
-        if not t.is_cuda:
-            _refuse(call, f"{name}: expected a CUDA tensor, got one on {t.device}")
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-            _refuse(call, f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if not t.is_contiguous():
-            _refuse(call, f"{name}: expected a contiguous tensor, got strides {t.stride()}")
-        if t.device != device:
-            _refuse(call, f"{name}: expected a tensor on {device}, got one on {t.device}")
-        out.append(t.data_ptr())
-    return out
+def _device_of(call, name, t):
+    """Index of the CUDA device the call's tensors have to be on."""
+    d = t.get_device()
+    if d < 0:
+        _refuse(call, f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return d
 
 
-def _on_device(call, device, stream, fn):
-    """fn(stream) with `device` current, on `stream` or the current stream of that device."""
-    import torch
+def _dense(call, device, name, t, dtype, shape):
+    """Address of a tensor (None passes through).  The library takes dense tensors and trusts their sizes, so it has
+    to be a contiguous tensor of that type and shape on CUDA device `device`."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        _refuse(call, f"{name}: expected a tensor on cuda:{device}, got one on {t.device}")
+    if t.dtype is not dtype or t.shape != shape:
+        _refuse(call, f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _refuse(call, f"{name}: expected a contiguous tensor, got strides {t.stride()}")
+    return t.data_ptr()
 
+
+def _on_device(call, device, stream, fn, *args):
+    """fn(*args, stream) with `device` current, on `stream` or the current stream of that device."""
+    cuda = _torch().cuda
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        _refuse(call, f"the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(stream.cuda_stream)
+        stream = cuda.current_stream(device)
+    elif stream.device.index != device:
+        _refuse(call, f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    if cuda.current_device() == device:
+        rc = fn(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(stream.cuda_stream)
-    _check(call, rc)
+        with cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != HISA_OK:
+        raise HisaError(call, rc)
 
 
-def _status_and_workspace(call, device, dev_status, workspace, nbytes):
-    import torch
-
+def _scratch(call, device, workspace, nbytes):
+    """(tensor, address) of the caller's workspace, or of a new one of nbytes() bytes."""
     if workspace is None:
-        workspace = _workspace(nbytes, device)
-    st, ws = _checked(call, device, dev_status=(dev_status, torch.int32, (1,)),
-                      workspace=(workspace, torch.uint8, (workspace.numel(),)))
-    return st, ws, workspace
+        workspace = _workspace(nbytes(), _torch().device("cuda", device))
+    return workspace, _dense(call, device, "workspace", workspace, _torch().uint8, (workspace.numel(),))
 
 
 def hisa_tree_attn_workspace_size(p, with_weight=False) -> int:
@@ -416,19 +426,18 @@ def hisa_tree_attn_fwd(p, q, k, v, kv_len, o, lse=None, parent=None, weight=None
     """Attention of p.n_q drafted tokens per sequence over a cache of p.n_kv rows (see include/hisa.h): q, o
     [b][n_q][H][d] and k, v [b][n_kv][Hk][d] bf16, kv_len [b] and parent [b][n_q] int32, lse [b][n_q][H] and
     weight [b][n_kv] fp32."""
-    import torch
-
-    call, dev = "hisa_tree_attn_fwd", q.device
+    torch, call = _torch(), "hisa_tree_attn_fwd"
+    dev = _device_of(call, "q", q)
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    qs, ks = (p.batch, p.n_q, p.n_heads, p.d_head), (p.batch, p.n_kv, p.n_kv_heads, p.d_head)
-    a = _checked(call, dev, q=(q, bf, qs), k=(k, bf, ks), v=(v, bf, ks), kv_len=(kv_len, i32, (p.batch,)),
-                 parent=(parent, i32, (p.batch, p.n_q)), o=(o, bf, qs), lse=(lse, f32, qs[:3]),
-                 weight=(weight, f32, ks[:2]))
-    st, ws, workspace = _status_and_workspace(
-        call, dev, dev_status, workspace,
-        hisa_tree_attn_workspace_size(p, weight is not None) if workspace is None else 0)
-    _on_device(call, dev, stream,
-               lambda s: _lib.hisa_tree_attn_fwd(ctypes.byref(p), *a, st, ws, workspace.numel(), s))
+    b, T, n, H, d = p.batch, p.n_q, p.n_kv, p.n_heads, p.d_head
+    ks = (b, n, p.n_kv_heads, d)
+    at = (_dense(call, dev, "q", q, bf, (b, T, H, d)), _dense(call, dev, "k", k, bf, ks),
+          _dense(call, dev, "v", v, bf, ks), _dense(call, dev, "kv_len", kv_len, i32, (b,)),
+          _dense(call, dev, "parent", parent, i32, (b, T)), _dense(call, dev, "o", o, bf, (b, T, H, d)),
+          _dense(call, dev, "lse", lse, f32, (b, T, H)), _dense(call, dev, "weight", weight, f32, (b, n)),
+          _dense(call, dev, "dev_status", dev_status, i32, (1,)))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_tree_attn_workspace_size(p, weight is not None))
+    _on_device(call, dev, stream, _lib.hisa_tree_attn_fwd, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
 def hisa_cache_weight_workspace_size(p) -> int:
@@ -439,18 +448,16 @@ def hisa_cache_weight(p, q, k, kv_len, lse, weight, parent=None, path=None, dev_
                       stream=None):
     """The attention weight each cached row receives from the counted slots, into weight [b][n_kv] (see
     include/hisa.h); path [b][n_q] int32: the accepted slots, ascending, -1 padded."""
-    import torch
-
-    call, dev = "hisa_cache_weight", q.device
+    torch, call = _torch(), "hisa_cache_weight"
+    dev = _device_of(call, "q", q)
     bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    qs, ks = (p.batch, p.n_q, p.n_heads, p.d_head), (p.batch, p.n_kv, p.n_kv_heads, p.d_head)
-    a = _checked(call, dev, q=(q, bf, qs), k=(k, bf, ks), kv_len=(kv_len, i32, (p.batch,)),
-                 parent=(parent, i32, (p.batch, p.n_q)), path=(path, i32, (p.batch, p.n_q)), lse=(lse, f32, qs[:3]),
-                 weight=(weight, f32, ks[:2]))
-    st, ws, workspace = _status_and_workspace(call, dev, dev_status, workspace,
-                                              hisa_cache_weight_workspace_size(p) if workspace is None else 0)
-    _on_device(call, dev, stream,
-               lambda s: _lib.hisa_cache_weight(ctypes.byref(p), *a, st, ws, workspace.numel(), s))
+    b, T, n, H, d = p.batch, p.n_q, p.n_kv, p.n_heads, p.d_head
+    at = (_dense(call, dev, "q", q, bf, (b, T, H, d)), _dense(call, dev, "k", k, bf, (b, n, p.n_kv_heads, d)),
+          _dense(call, dev, "kv_len", kv_len, i32, (b,)), _dense(call, dev, "parent", parent, i32, (b, T)),
+          _dense(call, dev, "path", path, i32, (b, T)), _dense(call, dev, "lse", lse, f32, (b, T, H)),
+          _dense(call, dev, "weight", weight, f32, (b, n)), _dense(call, dev, "dev_status", dev_status, i32, (1,)))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_weight_workspace_size(p))
+    _on_device(call, dev, stream, _lib.hisa_cache_weight, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
 def hisa_cache_keep_workspace_size(p) -> int:
@@ -461,37 +468,36 @@ def hisa_cache_keep(p, weight, kv_len, budget, keep_idx, kept_len, n_first=0, n_
                     workspace=None, stream=None):
     """The rows of each sequence to keep within `budget` (see include/hisa.h): keep_idx [b][budget] int32,
     ascending, -1 padded, and kept_len [b] int32, from weight [b][n_kv] fp32."""
-    import torch
-
-    call, dev, i32 = "hisa_cache_keep", weight.device, torch.int32
-    w, n, ki, kl = _checked(call, dev, weight=(weight, torch.float32, (p.batch, p.n_kv)),
-                            kv_len=(kv_len, i32, (p.batch,)), keep_idx=(keep_idx, i32, (p.batch, budget)),
-                            kept_len=(kept_len, i32, (p.batch,)))
-    st, ws, workspace = _status_and_workspace(call, dev, dev_status, workspace,
-                                              hisa_cache_keep_workspace_size(p) if workspace is None else 0)
-    _on_device(call, dev, stream,
-               lambda s: _lib.hisa_cache_keep(ctypes.byref(p), w, n, budget, n_first, n_recent, ki, kl, st, ws,
-                                              workspace.numel(), s))
+    torch, call = _torch(), "hisa_cache_keep"
+    dev = _device_of(call, "weight", weight)
+    i32, b = torch.int32, p.batch
+    at = (_dense(call, dev, "weight", weight, torch.float32, (b, p.n_kv)),
+          _dense(call, dev, "kv_len", kv_len, i32, (b,)), budget, n_first, n_recent,
+          _dense(call, dev, "keep_idx", keep_idx, i32, (b, budget)),
+          _dense(call, dev, "kept_len", kept_len, i32, (b,)), _dense(call, dev, "dev_status", dev_status, i32, (1,)))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_keep_workspace_size(p))
+    _on_device(call, dev, stream, _lib.hisa_cache_keep, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
 def hisa_cache_compact(p, rows, arrays, dst_begin=None, dev_status=None, stream=None):
     """Rows rows[s][j] of every array moved to dst_begin[s] + j, in place (see include/hisa.h).  arrays: tensors
     [b][n_kv][...] of any types whose rows have a multiple of 4 bytes."""
-    import torch
-
-    call, dev, i32 = "hisa_cache_compact", rows.device, torch.int32
+    torch, call = _torch(), "hisa_cache_compact"
+    dev = _device_of(call, "rows", rows)
+    i32, b, n_kv = torch.int32, p.batch, p.n_kv
     if rows.dim() != 2 or not 1 <= len(arrays) <= MAX_ROW_ARRAYS:
         _refuse(call, f"expected rows [b][n] and 1 to {MAX_ROW_ARRAYS} arrays, got {tuple(rows.shape)} and "
                       f"{len(arrays)}")
-    lead = (p.batch, p.n_kv)
-    r, d, st = _checked(call, dev, rows=(rows, i32, (p.batch, rows.shape[1])),
-                        dst_begin=(dst_begin, i32, (p.batch,)), dev_status=(dev_status, i32, (1,)))
+    n = rows.shape[1]
     c = (HisaRows * len(arrays))()
     for i, t in enumerate(arrays):
-        c[i].base, = _checked(call, dev, **{f"arrays[{i}]": (t, t.dtype, lead + tuple(t.shape[2:]))})
-        c[i].row_bytes = math.prod(t.shape[2:]) * t.element_size()
-    _on_device(call, dev, stream,
-               lambda s: _lib.hisa_cache_compact(ctypes.byref(p), r, rows.shape[1], d, c, len(arrays), st, s))
+        inner = t.shape[2:]
+        c[i].base = _dense(call, dev, f"arrays[{i}]", t, t.dtype, (b, n_kv, *inner))
+        c[i].row_bytes = math.prod(inner) * t.element_size()
+    _on_device(call, dev, stream, _lib.hisa_cache_compact, ctypes.byref(p),
+               _dense(call, dev, "rows", rows, i32, (b, n)), n,
+               _dense(call, dev, "dst_begin", dst_begin, i32, (b,)), c, len(arrays),
+               _dense(call, dev, "dev_status", dev_status, i32, (1,)))
 
 
 def hisa_gather_probe(rows, row_bytes, n_gathers, sink, seed=1, ctas_per_sm=0, stream=None):

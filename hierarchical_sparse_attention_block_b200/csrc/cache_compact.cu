@@ -5,11 +5,11 @@
 // In place, a destination row may be the source of another entry.  Every source is at or behind its
 // own destination and the sources ascend, so a sweep over j in ascending order that has read the
 // rows of entries [0, j1) may write the destinations [0, j1): a later entry's source lies at
-// begin + j1 or behind.  One CTA therefore owns a slice of at most 128 bytes of every row of one
-// sequence and sweeps the list in tiles: it loads the next tile's rows into registers, passes a
-// barrier (every load of the current tile is then in), and writes the current tile.  CTAs share no
-// byte, so nothing else has to be ordered.  The bound is HBM: each moved byte is read and written
-// once; the next tile's loads are in flight while the current one is stored.
+// begin + j1 or behind.  One CTA therefore owns a slice (128 bytes) of every row of one sequence and
+// sweeps the list in tiles: it loads the next tile's rows into registers, passes a barrier (every load
+// of the current tile is then in), and writes the current tile.  CTAs share no byte, so nothing else
+// has to be ordered.  The bound is HBM: each moved byte is read and written once; the next tile's
+// loads are in flight while the current one is stored.
 #include "common.cuh"
 #include "internal.h"
 
@@ -18,14 +18,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 8;    // row loads in flight per thread and tile
-constexpr int kLanesMax = 8;  // threads per row slice
+constexpr int kLanesMax = 8, kLanesShort = 64;  // threads per row slice: long lists, lists of one tile
 
 struct Array {
   uint8_t* base;
   int64_t row_bytes;
   int first_slice;  // first slice id of this array
   int vec;          // bytes per access: 16, or 4 where the rows are no multiple of 16
-  int lanes;        // threads per row slice: a power of two up to kLanesMax
+  int lanes;        // threads per row slice, a power of two
 };
 struct Arrays {
   Array a[kMaxRowArrays];
@@ -40,7 +40,7 @@ __device__ __forceinline__ V load_once(const uint8_t* p) {
 
 // The entries of one tile, checked: src[j] = the source row, or -1 for an entry that moves nothing.
 struct Tile {
-  int32_t src[kThreads * kUnroll];
+  int32_t src[kThreads * kUnroll];  // a row a thread at the most
 };
 
 template <class V>
@@ -171,8 +171,12 @@ cudaError_t launch_cache_compact(const Shape& s, const int32_t* rows, int n_rows
     A.row_bytes = arrays[i].row_bytes;
     A.vec = A.row_bytes % 16 == 0 ? 16 : 4;
     const int64_t units = A.row_bytes / A.vec;
+    // Long lists: slices of 128 bytes, so that even one sequence's sweeps cover the SMs.  A list that
+    // is one tile all the same takes wider ones: fewer CTAs, each of a few rows.
     A.lanes = 1;
-    while (A.lanes < kLanesMax && A.lanes < units) A.lanes *= 2;
+    while (A.lanes < units &&
+           (A.lanes < kLanesMax || (A.lanes < kLanesShort && (int64_t)kThreads / (2 * A.lanes) * kUnroll >= n_rows)))
+      A.lanes *= 2;
     A.first_slice = (int)slices;
     slices += (units + A.lanes - 1) / A.lanes;
   }

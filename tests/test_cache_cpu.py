@@ -112,6 +112,9 @@ class _OnGpu:
         self.shape, self.dtype, self.device, self.is_cuda = torch.Size(shape), dtype, torch.device(device), True
         self._c = contiguous
 
+    def get_device(self):
+        return self.device.index
+
     def is_contiguous(self):
         return self._c
 
