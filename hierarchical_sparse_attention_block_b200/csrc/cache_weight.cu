@@ -56,9 +56,9 @@ struct Cfg {
   static constexpr int KS = D == 64 ? 8 : 4;  // K ring
   static constexpr int K_OFF = 2 * kTile;     // Q buffer b at b * kTile (kQRows rows)
   static constexpr int TREE_OFF = K_OFF + KS * kTile;
-  static constexpr int ROW_OFF = (TREE_OFF + (int)sizeof(DraftTree) + 15) / 16 * 16;  // Rows [2]
-  static constexpr int LIST_OFF = ROW_OFF + 2 * (int)sizeof(Rows);                    // counted slots: int16 [kMaxDraft]
-  static constexpr int BAR_OFF = LIST_OFF + 2 * kMaxDraft;
+  static constexpr int ROW_OFF = (TREE_OFF + 2 * (int)sizeof(DraftTree) + 15) / 16 * 16;  // Rows [2]
+  static constexpr int LIST_OFF = ROW_OFF + 2 * (int)sizeof(Rows);  // counted slots: int16 [2][kMaxDraft]
+  static constexpr int BAR_OFF = LIST_OFF + 2 * 2 * kMaxDraft;
   enum : int {
     B_KFULL = 0,             // [KS]
     B_KEMPTY = B_KFULL + KS, // [KS]
@@ -66,15 +66,16 @@ struct Cfg {
     B_QEMPTY = B_QFULL + 2,  // [2]
     B_SFULL = B_QEMPTY + 2,  // [4]
     B_SFREE = B_SFULL + 4,   // [4]
-    B_SEGFULL = B_SFREE + 4, // the segment's slots and tree are there
-    B_SEGFREE,               // ... and read out
-    B_LSYNC,                 // the loader warps among themselves
+    B_SEGFULL = B_SFREE + 4,     // [2]: a segment's slots and tree are there
+    B_SEGFREE = B_SEGFULL + 2,   // [2]: ... and read out
+    B_GO = B_SEGFREE + 2,        // the first query rows are asked for
+    B_LSYNC,                     // the loader warps among themselves
     B_DRAIN,
     kNBar
   };
   static constexpr int WALK_OFF = BAR_OFF + kNBar * 8;
   static constexpr int MISC_OFF = WALK_OFF + (int)sizeof(WalkShared<kThreads>);
-  static constexpr int kSmem = MISC_OFF + 4 * (3 + 2 * kDraftWords) + 1024;
+  static constexpr int kSmem = MISC_OFF + 4 * 4 + 1024;
   static_assert(BAR_OFF % 8 == 0 && kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -82,9 +83,9 @@ struct Cfg {
 struct Chunks {
   int h0, nh, R, subs, heads, chunks;
   __device__ Chunks(int h0_, int nh_, int R_) : h0(h0_), nh(nh_), R(R_) {
-    subs = max(1, (R + kQRows - 1) / kQRows);              // fills of one head
-    heads = R == 0 ? 1 : max(1, kQRows / ((R + 15) & ~15));  // heads of one fill
-    chunks = R == 0 ? 0 : subs == 1 ? (nh + heads - 1) / heads : nh * subs;
+    subs = max(1, (R + kQRows - 1) / kQRows);                     // fills of one head
+    heads = min(nh, max(1, kQRows / max(16, (R + 15) & ~15)));  // heads of one fill
+    chunks = subs == 1 ? (nh + heads - 1) / heads : nh * subs;
   }
   // fill c: heads [head, head + n), rows [row0, row0 + rows) of each, at pitch `pitch` in the buffer
   int head, n, row0, rows, pitch;
@@ -100,7 +101,7 @@ struct Chunks {
       row0 = c % subs * kQRows;
       rows = min(kQRows, R - row0);
     }
-    pitch = (rows + 15) & ~15;
+    pitch = max(16, (rows + 15) & ~15);  // nothing counted: padding alone
   }
 };
 
@@ -117,18 +118,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) { return sb + (uint32_t)C::BAR_OFF + 8u * (uint32_t)i; };
-  DraftTree& tree = *reinterpret_cast<DraftTree*>(smem + C::TREE_OFF);
+  DraftTree* trees = reinterpret_cast<DraftTree*>(smem + C::TREE_OFF);  // [2]: of the segments in turn, as the lists
   Rows* rows_of = reinterpret_cast<Rows*>(smem + C::ROW_OFF);
-  int16_t* list = reinterpret_cast<int16_t*>(smem + C::LIST_OFF);
+  int16_t* lists = reinterpret_cast<int16_t*>(smem + C::LIST_OFF);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* n_counted = reinterpret_cast<volatile int*>(misc + 2);
+  volatile int* n_counted = reinterpret_cast<volatile int*>(misc + 2);  // [2]
   auto fail = [&]() {
     *abort_flag = 1;
     if (status) atomicOr(status, kStatusTimeout);
   };
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int G = H / Hkv;
+  const bool wide = T * G > kQRows;  // how often K is read depends on the counted slots
   if (warp == kWarpMMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols));
@@ -140,8 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= C::B_QFULL && i < C::B_QEMPTY) n = kLoaders;
       if (i >= C::B_QEMPTY && i < C::B_SFULL) n = kReadout + 1;
       if (i >= C::B_SFREE && i < C::B_SEGFULL) n = kKeys;
-      if (i == C::B_SEGFULL || i == C::B_LSYNC) n = kLoaders;
-      if (i == C::B_SEGFREE) n = kReadout + 2;  // and the K and MMA threads
+      if ((i >= C::B_SEGFULL && i < C::B_SEGFREE) || i == C::B_GO || i == C::B_LSYNC) n = kLoaders;
+      if (i >= C::B_SEGFREE && i < C::B_GO) n = kReadout + (wide ? 2 : 1);  // and the MMA thread, the K thread
       mbar_init(bar(i), (uint32_t)n);
     }
     *abort_flag = 0;
@@ -153,10 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), nullptr, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int G = H / Hkv;
-  auto chunks_of = [&](int item) {  // item: the group of KV heads
+  auto chunks_of = [&](int item, int rows) {  // item: the group of KV heads; rows: query rows of a head
     const int h0 = (int)((int64_t)item * Hkv / groups), h1 = (int)((int64_t)(item + 1) * Hkv / groups);
-    return Chunks(h0, h1 - h0, *n_counted * G);
+    return Chunks(h0, h1 - h0, rows);
   };
 
   if (warp >= kWarpQ && warp < kWarpK) {
@@ -171,9 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       lphase ^= 1u;
     };
     while (ok && walk.next()) {
+      // one segment ahead of the readout
       const int64_t seq = walk.s;
-      if (seg > 0) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFREE), (uint32_t)(seg - 1) & 1u, abort_flag));
+      const int sp = seg & 1;
+      DraftTree& tree = trees[sp];
+      int16_t* list = lists + sp * kMaxDraft;
+      if (seg >= 2) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFREE + sp), (uint32_t)((seg >> 1) - 1) & 1u, abort_flag));
         if (!ok) break;
       }
       bool bad = false;
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             if ((keep >> x) & 1u) list[at++] = (int16_t)e[x];
-          if (lane == 0) *n_counted = all;
+          if (lane == 0) n_counted[sp] = all;
         } else {
           int n = 0;
           for (int i0 = 0; i0 < T; i0 += 32) {
@@ -238,15 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c) list[n + __popc(b & ((1u << lane) - 1u))] = (int16_t)i;
             n += __popc(b);
           }
-          if (lane == 0) *n_counted = n;
+          if (lane == 0) n_counted[sp] = n;
         }
       }
       if (bad && status) atomicOr(status, kStatusBadIndex);
       sync();
       if (!ok) break;
-      mbar_arrive(bar(C::B_SEGFULL));
+      mbar_arrive(bar(C::B_SEGFULL + sp));
       ++seg;
-      Chunks ch = chunks_of(walk.item);
+      Chunks ch = chunks_of(walk.item, n_counted[sp] * G);
       for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
         ch.at(c);
         const int b = fill & 1;
@@ -283,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows.nlse2[lt] = nl;
           rows.slot[lt] = (int16_t)slot;
         }
+        if (fill == 0) mbar_arrive(bar(C::B_GO));
         cp_async_wait<0>();
         fence_async_smem();
         mbar_arrive(bar(C::B_QFULL + b));
@@ -297,17 +304,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t policy = l2_evict_first();
       int seg = 0, issued = 0;
       while (ok && walk.next()) {
-        ok = mbar_wait_or_abort(bar(C::B_SEGFULL), (uint32_t)seg & 1u, abort_flag);
-        ++seg;
-        if (!ok) break;
-        Chunks ch = chunks_of(walk.item);
-        mbar_arrive(bar(C::B_SEGFREE));
+        int rows = 0;  // any number up to kQRows passes the group's heads in one fill
+        if (wide) {
+          ok = mbar_wait_or_abort(bar(C::B_SEGFULL + (seg & 1)), (uint32_t)(seg >> 1) & 1u, abort_flag);
+          if (!ok) break;
+          rows = n_counted[seg & 1] * G;
+          mbar_arrive(bar(C::B_SEGFREE + (seg & 1)));
+          ++seg;
+        }
+        Chunks ch = chunks_of(walk.item, rows);
         for (int c = 0; ok && c < ch.chunks; ++c) {
           ch.at(c);
           for (int x = 0; ok && x < walk.n; x += 2)
             for (int hd = 0; ok && hd < ch.n; ++hd)
               for (int e = 0; e < 2 && x + e < walk.n; ++e) {
                 const int s = issued % C::KS;
+                // The first query rows go before all but one K tile: behind the first tiles of every SM
+                // they would wait for all of those.
+                if (issued == 1 && !mbar_wait_or_abort(bar(C::B_GO), 0, abort_flag)) {
+                  ok = false;
+                  break;
+                }
                 if (issued >= C::KS &&
                     !mbar_wait_or_abort(bar(C::B_KEMPTY + s), (uint32_t)(issued / C::KS - 1) & 1u, abort_flag)) {
                   ok = false;
@@ -335,11 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seg = 0, fill = 0, kit = 0;
       int made[2] = {0, 0};  // products handed to each readout group
       while (ok && walk.next()) {
-        ok = mbar_wait_or_abort(bar(C::B_SEGFULL), (uint32_t)seg & 1u, abort_flag);
-        ++seg;
+        ok = mbar_wait_or_abort(bar(C::B_SEGFULL + (seg & 1)), (uint32_t)(seg >> 1) & 1u, abort_flag);
         if (!ok) break;
-        Chunks ch = chunks_of(walk.item);
-        mbar_arrive(bar(C::B_SEGFREE));
+        Chunks ch = chunks_of(walk.item, n_counted[seg & 1] * G);
+        mbar_arrive(bar(C::B_SEGFREE + (seg & 1)));
+        ++seg;
         for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
           ch.at(c);
           const int qb = fill & 1;
@@ -383,21 +400,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int seg = 0, fill = 0, got = 0;
     while (ok && walk.next()) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFULL), (uint32_t)seg & 1u, abort_flag));
+      const int sp = seg & 1;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFULL + sp), (uint32_t)(seg >> 1) & 1u, abort_flag));
       ++seg;
       if (!ok) break;
+      const DraftTree& tree = trees[sp];
       const int64_t seq = walk.s;
       const int L = (int)walk.L;
-      Chunks ch = chunks_of(walk.item);
+      Chunks ch = chunks_of(walk.item, n_counted[sp] * G);
       float* out = groups == 1 ? weight + seq * n_kv : part + ((int64_t)walk.item * batch + seq) * n_kv;
-      // One fill's sum of a key joins what the fills before left; nothing counted leaves 0.
+      // One fill's sum of a key joins what the fills before left.
       auto add = [&](int c, int t, float sum) {
         if (t >= L + T) return;
         if (c > 0 || (groups == 1 && t < L)) sum += out[t];
         out[t] = sum;
       };
-      if (ch.chunks == 0)
-        for (int x = e; x < walk.n; x += 2) add(0, (walk.j0 + x) * kKeys + r, 0.f);
       for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
         ch.at(c);
         const int qb = fill & 1;
@@ -465,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_arrive(bar(C::B_QEMPTY + qb));
       }
-      mbar_arrive(bar(C::B_SEGFREE));
+      mbar_arrive(bar(C::B_SEGFREE + sp));
     }
     if (!ok && lane == 0) fail();
   }
