@@ -48,6 +48,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Rows {
   float nlse2[kQRows];
   int16_t slot[kQRows];
+  uint32_t none[kQRows / 32];  // bit per row: padding, or a row that adds nothing
 };
 
 template <int D>
@@ -276,9 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         cp_async_commit();
         Rows& rows = rows_of[b];
+        float nl = -INFINITY;
         if (lt < total) {
           const int hd = lt / ch.pitch, rr = lt - hd * ch.pitch;
-          float nl = -INFINITY;
           int slot = 0;
           if (rr < ch.rows) {
             const int r = ch.row0 + rr, ci = r / G;
@@ -289,6 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           rows.nlse2[lt] = nl;
           rows.slot[lt] = (int16_t)slot;
         }
+        const uint32_t none = __ballot_sync(0xFFFFFFFFu, nl == -INFINITY);
+        if (lane == 0) rows.none[lt >> 5] = none;
         if (fill == 0) mbar_arrive(bar(C::B_GO));
         cp_async_wait<0>();
         fence_async_smem();
@@ -433,45 +436,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int first = hd * ch.pitch;
             const float2 qs2 = {qscale, qscale};
             float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            for (int c0 = 0; c0 < ch.pitch; c0 += 32) {
-              // 32 columns (the last block may reach behind the pitch, within the score buffer)
-              uint32_t s[32];
-              __syncwarp();  // the load takes the whole warp
-              tmem_ld32_issue(ts + 128u * (uint32_t)buf + (uint32_t)c0, s);
-              tmem_wait_ld(s);
+            const uint32_t tb = ts + 128u * (uint32_t)buf;
+            auto take = [&](int c0, uint32_t(&s)[32]) {  // columns c0 .. c0 + 31, those below the pitch
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
+                const int at = first + c0 + 16 * h;
                 if (c0 + 16 * h >= ch.pitch) break;
                 float nl[16];
 #pragma unroll
                 for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<float4*>(nl + i) = *reinterpret_cast<const float4*>(rows.nlse2 + first + c0 + 16 * h + i);
-                if (c0 + 16 * h + 16 <= ch.rows && !tail) {
-                  bool none = false;
+                  *reinterpret_cast<float4*>(nl + i) = *reinterpret_cast<const float4*>(rows.nlse2 + at + i);
+                const uint32_t none = rows.none[at >> 5] >> (at & 16) & 0xFFFFu;
+                if (none == 0 && !tail) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) none = none || nl[i] == -INFINITY;
-                  if (!none) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                      const float2 x = ffma2(make_float2(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])),
-                                             qs2, make_float2(nl[2 * i], nl[2 * i + 1]));
-                      acc[i & 1] = fadd2(acc[i & 1], make_float2(fast_exp2(x.x), fast_exp2(x.y)));
-                    }
-                    continue;
+                  for (int i = 0; i < 8; ++i) {
+                    const float2 x = ffma2(make_float2(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])),
+                                           qs2, make_float2(nl[2 * i], nl[2 * i + 1]));
+                    acc[i & 1] = fadd2(acc[i & 1], make_float2(fast_exp2(x.x), fast_exp2(x.y)));
                   }
+                  continue;
                 }
-                // padding, rows that add nothing (-inf), and what a drafted row is not seen by
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  bool see = nl[i] != -INFINITY;
-                  if (tail && j >= 0) {
-                    const int slot = rows.slot[first + c0 + 16 * h + i];
+                  bool see = !((none >> i) & 1u);
+                  if (tail && j >= 0) {  // a drafted row: only the slots below it in the tree see it
+                    const int slot = rows.slot[at + i];
                     see = see && (parent ? j < T && ((tree.anc[slot][j >> 5] >> (j & 31)) & 1u) : j <= slot);
                   }
                   const float p = fast_exp2(fmaf(__uint_as_float(s[16 * h + i]), qscale, nl[i]));
-                  acc[0].x += see ? p : 0.f;
+                  acc[i & 1].x += see ? p : 0.f;
                 }
               }
+            };
+#pragma unroll 1
+            for (int c0 = 0; c0 < ch.pitch; c0 += 32) {  // a load may reach behind the pitch, within the buffer
+              uint32_t x[32];
+              __syncwarp();
+              tmem_ld32_issue(tb + (uint32_t)c0, x);
+              tmem_wait_ld(x);
+              take(c0, x);
             }
             tc_fence_before();
             mbar_arrive(bar(C::B_SFREE + 2 * e + buf));
