@@ -350,20 +350,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    {
+      auto waited = [&](uint32_t barrier, uint32_t parity) {  // the warp stays together
+        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(barrier, parity, abort_flag)) != 0;
+      };
       bool ok = true;
       int seg = 0, fill = 0, kit = 0;
       int made[2] = {0, 0};  // products handed to each readout group
       while (ok && walk.next()) {
-        ok = mbar_wait_or_abort(bar(C::B_SEGFULL + (seg & 1)), (uint32_t)(seg >> 1) & 1u, abort_flag);
+        ok = waited(bar(C::B_SEGFULL + (seg & 1)), (uint32_t)(seg >> 1) & 1u);
         if (!ok) break;
         Chunks ch = chunks_of(walk.item, n_counted[seg & 1] * G);
-        mbar_arrive(bar(C::B_SEGFREE + (seg & 1)));
+        if (lane == 0) mbar_arrive(bar(C::B_SEGFREE + (seg & 1)));
         ++seg;
         for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
           ch.at(c);
           const int qb = fill & 1;
-          ok = mbar_wait_or_abort(bar(C::B_QFULL + qb), (uint32_t)(fill >> 1) & 1u, abort_flag);
+          ok = waited(bar(C::B_QFULL + qb), (uint32_t)(fill >> 1) & 1u);
           const uint32_t idesc = idesc_bf16(kKeys, ch.pitch, false, false);
           for (int x = 0; ok && x < walk.n; x += 2)
             for (int hd = 0; ok && hd < ch.n; ++hd)
@@ -371,13 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 2; ++e) {
                 if (!ok || x + e >= walk.n) continue;
                 const int s = kit % C::KS, buf = 2 * e + (made[e] & 1);
-                ok = mbar_wait_or_abort(bar(C::B_KFULL + s), (uint32_t)(kit / C::KS) & 1u, abort_flag) &&
+                ok = waited(bar(C::B_KFULL + s), (uint32_t)(kit / C::KS) & 1u) &&
                      (made[e] < 2 ||
-                      mbar_wait_or_abort(bar(C::B_SFREE + buf), (uint32_t)((made[e] >> 1) - 1) & 1u, abort_flag));
+                      waited(bar(C::B_SFREE + buf), (uint32_t)((made[e] >> 1) - 1) & 1u));
                 if (!ok) continue;
                 tc_fence_after();
                 const uint32_t kt = sb + (uint32_t)(C::K_OFF + s * C::kTile);
                 const uint32_t qt = sb + (uint32_t)(qb * C::kTile + hd * ch.pitch * 128);
+                if (elect_one()) {
 #pragma unroll
                 for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
@@ -386,14 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                               desc_kmajor_sw128(qt + h2 * kHalf + kk * 32), idesc, (h2 | kk) ? 1u : 0u);
                 umma_commit(bar(C::B_SFULL + buf));
                 umma_commit(bar(C::B_KEMPTY + s));
+                }
                 ++made[e];
                 ++kit;
               }
-          if (ok) umma_commit(bar(C::B_QEMPTY + qb));
+          if (ok && elect_one()) umma_commit(bar(C::B_QEMPTY + qb));
         }
       }
-      if (!ok) fail();
-      umma_commit(bar(C::B_DRAIN));
+      if (!ok && lane == 0) fail();
+      if (elect_one()) umma_commit(bar(C::B_DRAIN));
       mbar_wait(bar(C::B_DRAIN), 0);
     }
   } else {

@@ -16,21 +16,20 @@
 // SM.  An item that one CTA holds whole is written by it; the others leave (max, sum, unnormalised
 // output) per range in the workspace, merged by tree_attn_merge_kernel.
 //
+// This file's kernel takes 65 query rows and more of a KV head, one or two tiles of 128 rows at a time;
+// tree_attn_few.cu up to 64, with the keys as the product's rows.
+//
 // Roles of a CTA: two softmax groups of four warps, one thread per query row (TMEM lane = row); then
 // one thread each for the K loads (TMA), the MMAs (tcgen05) and the V loads.  Two row tiles: each
 // group has its tile.  One row tile: the groups take the key tiles in turn, each with its own running
 // max, sum and output, joined at the segment's end; a group's softmax takes longer than a tile's
-// bytes, two side by side do not.  Up to 64 query rows (32) the tile holds them two (four) times, and
-// a warp forms the weights of half (a quarter) of the tile's keys for its copy, again with its own max
-// and sum: a row's 128 exponentials in one thread are what a group's time goes to.  Either way a
-// group's scores of the next tile follow the product with its weights of this one, and one group's
-// products run while the other's weights are formed.
+// bytes, two side by side do not.  Either way a group's scores of the next tile follow the product with
+// its weights of this one, and one group's products run while the other's weights are formed.
 // Scores and weights share columns of tensor memory: a row's scores are read 32 at a time, and its
-// weights written over them.  Up to 64 query rows, where the tensor cores have time, a weight enters as
-// two bf16 numbers (w = hi + lo to 16 significant bits), the A operands of two products with V.  With
-// more it is one: rounding the weights to 8 bits then moves an output of n comparable weights by about
-// as much as its own rounding to bf16 does, and the second product would cost up to a quarter of the
-// call (16 x 32K rows, 128 query rows a KV head: 210 us with it, 161 without).
+// weights written over them, as bf16: rounding the weights to 8 bits moves an output of n comparable
+// weights by about as much as its own rounding to bf16 does; a second product with the weights' low
+// parts took a quarter of the call (16 x 32K rows, 128 query rows a KV head: 210 us with it, 161
+// without).
 //
 // Rows that a slot does not see get weight 0 by a bit mask in the key tiles from L on; there, V rows
 // that no token holds are zeroed in shared memory, and values that are no finite numbers are taken out
@@ -38,25 +37,14 @@
 // Every wait is bounded (1 s): a timeout sets status bit 1 and the CTA stops.
 #include <math.h>
 
-#include <type_traits>
-
-#include "attn_math.cuh"
-#include "cache_walk.cuh"
-#include "common.cuh"
-#include "draft_tree.cuh"
-#include "internal.h"
-#include "tc_common.cuh"
+#include "tree_attn.cuh"
 
 namespace hisa {
 namespace {
 
 using namespace tc;
 
-constexpr int kRows = kTileKeys;  // query rows per tile = keys per key tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kHalf = kRows * 128;  // 64 columns of 128 rows of 16-bit values: one 128-byte swizzle span
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kSoftmax = 256;  // two groups
 constexpr int kThreads = kSoftmax + 96;
@@ -93,22 +81,16 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-// What the CTAs share with the merge: the unit ranges and the partial results.
-struct Work {
-  int64_t* prefix;  // [b + 1] key tiles of the sequences before; the total at the end
-  float4* part_o;   // [cta][2][D / 4][NT * 128]: four columns of a row; neighbours are rows
-  float2* part_ml;  // [cta][2][NT * 128]: max (log2 domain), sum; (+inf, 0): the row's slot is empty
-};
-
-template <int D, int NT, int REP>
+template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     const uint16_t* __restrict__ q, const uint16_t* __restrict__ v,
-                     const int32_t* __restrict__ kv_len, const int32_t* __restrict__ parent, uint16_t* __restrict__ o,
-                     float* __restrict__ lse, float* __restrict__ scores, int64_t score_stride, Work work,
-                     int32_t* __restrict__ status, int batch, int T, int64_t n_kv, int H, int Hkv, float qscale) {
-  static_assert(NT == 1 || REP == 1, "copies of the rows are for one row tile");
-  constexpr bool LO = REP > 1;  // weights as two bf16 numbers
+                     const __grid_constant__ TreeArgs args) {
+  const int32_t* const parent = args.parent;
+  int32_t* const status = args.status;
+  const Work& work = args.work;
+  const int T = args.T, H = args.H, Hkv = args.Hkv;
+  const int64_t n_kv = args.n_kv;
+  const float qscale = args.qscale;
   using C = Cfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -143,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   const int G = H / Hkv, R = T * G, np = (R + NT * kRows - 1) / (NT * kRows);  // items: (KV head, row-tile pair)
   tc_fence_before();
-  Walk walk = walk_begin<kThreads>(kv_len, n_kv, T, batch, Hkv * np,
+  Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv * np,
                                       *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -188,21 +170,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    {
+      auto waited = [&](uint32_t barrier, uint32_t parity) {  // the warp stays together
+        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(barrier, parity, abort_flag)) != 0;
+      };
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q and K both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // weights (tensor memory), V MN-major
-      constexpr int kParts = LO ? 2 : 1;                        // of a weight: high and low
       bool ok = true;
       int kit = 0, vit = 0, seg = 0;  // K and V tiles taken so far, segments
       int cnt[2] = {0, 0};            // products with the weights of each group
       auto wait_k = [&]() {
-        const bool r = mbar_wait_or_abort(bar(C::B_KFULL + kit % C::KS), (uint32_t)(kit / C::KS) & 1u, abort_flag);
+        const bool r = waited(bar(C::B_KFULL + kit % C::KS), (uint32_t)(kit / C::KS) & 1u);
         tc_fence_after();
         return r;
       };
       auto scores_of = [&](int t) {  // group t's scores with the K tile kit
         const uint32_t kt = sb + (uint32_t)(C::K_OFF + (kit % C::KS) * C::kTile);
         const uint32_t qb = sb + (uint32_t)(NT == 2 ? t * C::kTile : 0);
+        if (elect_one()) {
 #pragma unroll
         for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
@@ -210,37 +195,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_bf16(tmem + 128u * (uint32_t)t, desc_kmajor_sw128(qb + h2 * kHalf + kk * 32),
                       desc_kmajor_sw128(kt + h2 * kHalf + kk * 32), kIdS, (h2 | kk) ? 1u : 0u);
         umma_commit(bar(C::B_SFULL + t));
+        }
       };
       auto free_k = [&]() {
-        umma_commit(bar(C::B_KEMPTY + kit % C::KS));
+        if (elect_one()) umma_commit(bar(C::B_KEMPTY + kit % C::KS));
         ++kit;
       };
       auto output_of = [&](int t, bool first) {  // O_t += group t's weights x the V tile vit
         const uint32_t vt = sb + (uint32_t)(C::V_OFF + (vit % C::VS) * C::kTile);
+        if (elect_one()) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-          for (int kk = 0; kk < kRows / 16; ++kk)
-            umma_bf16_ta(tmem + col_o(t), tmem + 128u * (uint32_t)t + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1) + 16 * part),
-                         desc_mnmajor_sw128(vt + kk * 2048, kHalf), kIdO, (!first || part || kk) ? 1u : 0u);
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          umma_bf16_ta(tmem + col_o(t), tmem + 128u * (uint32_t)t + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1)),
+                       desc_mnmajor_sw128(vt + kk * 2048, kHalf), kIdO, (!first || kk) ? 1u : 0u);
         umma_commit(bar(C::B_PFREE + t));
+        }
         ++cnt[t];
       };
       auto wait_weights = [&](int t) {
-        const bool r = mbar_wait_or_abort(bar(C::B_PREADY + t), (uint32_t)cnt[t] & 1u, abort_flag);
+        const bool r = waited(bar(C::B_PREADY + t), (uint32_t)cnt[t] & 1u);
         tc_fence_after();
         return r;
       };
       auto wait_v = [&]() {
-        return mbar_wait_or_abort(bar(C::B_VFULL + vit % C::VS), (uint32_t)(vit / C::VS) & 1u, abort_flag);
+        return waited(bar(C::B_VFULL + vit % C::VS), (uint32_t)(vit / C::VS) & 1u);
       };
       auto free_v = [&]() {
-        umma_commit(bar(C::B_VEMPTY + vit % C::VS));
+        if (elect_one()) umma_commit(bar(C::B_VEMPTY + vit % C::VS));
         ++vit;
       };
       while (ok && walk.next()) {
         const int n = walk.n;
-        ok = mbar_wait_or_abort(bar(C::B_QFULL), (uint32_t)seg & 1u, abort_flag) && wait_k();
+        ok = waited(bar(C::B_QFULL), (uint32_t)seg & 1u) && wait_k();
         ++seg;
         if (!ok) break;
         if constexpr (NT == 1) {
@@ -295,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) fail();
-      umma_commit(bar(C::B_DRAIN));
+      if (!ok && lane == 0) fail();
+      if (elect_one()) umma_commit(bar(C::B_DRAIN));
       mbar_wait(bar(C::B_DRAIN), 0);
     }
   } else {
@@ -329,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nr > 0) {
         constexpr int CH = D / 8;  // 16-byte chunks of a row; rows that hold no query are 0
         for (int e = NT == 2 ? r : tid; e < kRows * CH; e += NT == 2 ? kRows : kSoftmax) {
-          const int row = e / CH, c = e % CH, qr = row % (kRows / REP);
-          const bool held = qr < nr;
-          const int i = (base + qr) / G, hg = (base + qr) - i * G;
+          const int row = e / CH, c = e % CH;
+          const bool held = row < nr;
+          const int i = (base + row) / G, hg = (base + row) - i * G;
           cp_async16(smem + (NT == 2 ? t * C::kTile : 0) + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                     held ? q + ((seq * T + i) * H + g * G + hg) * D + c * 8 : q, held);
+                     args.q + (held ? ((seq * T + i) * H + g * G + hg) * D + c * 8 : 0), held);
         }
         cp_async_commit();
       }
@@ -353,14 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vit0 = vit;
       vit += walk.n;
       if (NT == 2 && nr <= 0) continue;  // this group has no rows here
-      // This thread's query row of the tile, and its share of the tile's columns: blocks [cb, cb + kBlocks)
-      // of 32.
-      constexpr int kBlocks = 4 / REP;
-      const int qr = r % (kRows / REP), cb = r / (kRows / REP) * kBlocks;
-      const int slot_i = min(base + qr, R - 1) / G;  // drafted token of this row
+      const int slot_i = min(base + r, R - 1) / G;  // drafted token of this row
       // an empty slot; where the segment ends within the context, the merge learns it from another part
       const bool empty = treed && tree.end[slot_i] != kRoot;
-      const bool warp_rows = (qr & ~31) < nr;       // the warp has rows
+      const bool warp_rows = (r & ~31) < nr;        // the warp has rows
       float m_run = -INFINITY;                      // running max of the row's scores
       float2 l2 = {0.f, 0.f};                       // sum of the row's weights, relative to m_run
       bool any = false;                             // the group had a key tile
@@ -368,18 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = NT == 2 ? 0 : t; x < walk.n; x += NT == 2 ? 1 : 2, ++cnt) {
         const int t0 = (walk.j0 + x) * kRows;
         const bool tail = t0 + kRows > L;
-        if (t == 0 && x == ahead_at) {
-          // the next segment's query rows and tree are brought to the L2 meanwhile
-          Walk ahead = walk;
-          if (ahead.next()) {
-            const int g2 = ahead.item / np, base2 = NT == 2 ? (ahead.item - g2 * np) * 256 : 0;
-            for (int e = r; e < min(NT * kRows, R - base2) * (D / 64); e += kRows) {
-              const int rr = base2 + e / (D / 64), i = rr / G;
-              prefetch_l2(q + (((int64_t)ahead.s * T + i) * H + g2 * G + (rr - i * G)) * D + (e % (D / 64)) * 64);
-            }
-            if (parent && r * 32 < T) prefetch_l2(parent + (int64_t)ahead.s * T + r * 32);
-          }
-        }
+        if (t == 0 && x == ahead_at) prefetch_next<D>(walk, args, np, NT * kRows, r);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + t), (uint32_t)cnt & 1u, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -398,39 +369,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           auto look = [&](int c4, uint32_t(&x)[32]) {
             mask(c4, x);
-            if (NT == 1 && scores && qr < nr) {
-              float* out = scores + ((seq * Hkv + g) * R + qr) * score_stride + t0 + 32 * c4;
-#pragma unroll
-              for (int c = 0; c < 32; c += 4)
-                *reinterpret_cast<float4*>(out + c) =
-                    make_float4(__uint_as_float(x[c]) * qscale, __uint_as_float(x[c + 1]) * qscale,
-                                __uint_as_float(x[c + 2]) * qscale, __uint_as_float(x[c + 3]) * qscale);
-            }
-            __syncwarp();
 #pragma unroll
             for (int c = 0; c < 32; c += 2)
               m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           };
-          issue(cb, xa);
+          issue(0, xa);
           tmem_wait_ld(xa);
-          if constexpr (kBlocks == 1) {
-            look(cb, xa);
-          } else {
-            issue(cb + 1, xb);
-            look(cb, xa);
-            tmem_wait_ld(xb);
-            if constexpr (kBlocks == 4) {
-              issue(2, xa);
-              look(1, xb);
-              tmem_wait_ld(xa);
-              issue(3, xb);
-              look(2, xa);
-              tmem_wait_ld(xb);
-              look(3, xb);
-            } else {
-              look(cb + 1, xb);
-            }
-          }
+          issue(1, xb);
+          look(0, xa);
+          tmem_wait_ld(xb);
+          issue(2, xa);
+          look(1, xb);
+          tmem_wait_ld(xa);
+          issue(3, xb);
+          look(2, xa);
+          tmem_wait_ld(xb);
+          look(3, xb);
           const float tmax = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           // the max moves only when a weight would exceed 2^8
           const bool raise = tmax > m_run + lim;  // also the first visible key of the row (m_run = -inf)
@@ -447,44 +401,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float nmq = m_run == -INFINITY ? 0.f : -m_run * qscale;
           const float2 nmq2 = {nmq, nmq};
-          // the weights of a block over its scores: pairs (2 i, 2 i + 1), high parts in the block's columns
-          // 0-15, low parts in its columns 16-31
+          // the weights of a block over its scores: pairs (2 i, 2 i + 1) in the block's first 16 columns
           float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
           auto weigh = [&](int c4, const uint32_t(&x)[32]) {
-            uint32_t hi[16], lo[16];
+            uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float2 e = ffma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), qs2, nmq2);
               const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));  // 0 where masked
               ls[i & 1] = fadd2(ls[i & 1], p);
-              hi[i] = pack_bf16(p.x, p.y);
-              if (LO) lo[i] = pack_bf16(p.x - bf16_lo(hi[i]), p.y - bf16_hi(hi[i]));
+              w[i] = pack_bf16(p.x, p.y);
             }
-            tmem_st16_issue(ts + (uint32_t)(32 * c4), hi);
-            if (LO) tmem_st16_issue(ts + (uint32_t)(32 * c4 + 16), lo);
+            tmem_st16_issue(ts + (uint32_t)(32 * c4), w);
           };
-          if constexpr (kBlocks == 1) {
-            weigh(cb, xa);
-          } else if constexpr (kBlocks == 2) {
-            weigh(cb, xa);
-            weigh(cb + 1, xb);
-          } else {
-            weigh(2, xa);
-            issue(0, xa);
-            weigh(3, xb);
-            tmem_wait_ld(xa);
-            issue(1, xb);
-            mask(0, xa);
-            weigh(0, xa);
-            tmem_wait_ld(xb);
-            mask(1, xb);
-            weigh(1, xb);
-          }
-          if constexpr (REP > 1) {  // the other copies' columns count nothing here
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4)
-              if (c4 / kBlocks != cb / kBlocks) tmem_zero32_issue(ts + (uint32_t)(32 * c4));
-          }
+          weigh(2, xa);
+          issue(0, xa);
+          weigh(3, xb);
+          tmem_wait_ld(xa);
+          issue(1, xb);
+          mask(0, xa);
+          weigh(0, xa);
+          tmem_wait_ld(xb);
+          mask(1, xb);
+          weigh(1, xb);
           l2 = fadd2(l2, fadd2(ls[0], ls[1]));
           if (__any_sync(0xFFFFFFFFu, resc)) {  // the group's output holds earlier tiles: rescale it once they are in
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag))) {
@@ -509,35 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int vs = (vit0 + x) % C::VS;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)((vit0 + x) / C::VS) & 1u, abort_flag));
           if (!ok) break;
-          uint8_t* vt = smem + C::V_OFF + vs * C::kTile;
-          constexpr int CH = D / 8;
-          for (int e = max(0, L - t0) * CH + r; e < kRows * CH; e += kRows) {  // 16 bytes each, CH to a row
-            const int row = e / CH, c = e % CH, j = t0 + row - L;
-            const bool held = j < T && (!parent || tree.end[j] == kRoot);
-            uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + row * 128 + (c & 7) * 16);
-            if (!held) {
-              *p = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint4 w = *p;
-            uint32_t* a = reinterpret_cast<uint32_t*>(&w);
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((a[i] & 0x7F80u) == 0x7F80u) {
-                a[i] &= 0xFFFF0000u;
-                found = true;
-              }
-              if ((a[i] & 0x7F800000u) == 0x7F800000u) {
-                a[i] &= 0xFFFFu;
-                found = true;
-              }
-            }
-            if (found) {
-              *p = w;
-              atomicOr(&odd[j >> 5], 1u << (j & 31));
-            }
-          }
+          clear_tail_values<D>(smem + C::V_OFF + vs * C::kTile, t0, L, T, parent != nullptr, tree, odd, r);
           fence_async_smem();
           __syncwarp();
         }
@@ -553,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float l = l2.x + l2.y;
       float m = m_run == -INFINITY ? -INFINITY : m_run * qscale;  // log2 domain
-      // What this lane's two outputs count: w0 O_0 + w1 O_1; one row tile: both groups' key tiles and all
-      // copies of the row joined, each group taking half of the columns.
+      // What the row's two outputs count: w0 O_0 + w1 O_1; one row tile: both groups' key tiles joined, each
+      // group taking half of the columns.
       int c0 = 0, c1 = D;
       float w0 = t == 0 ? 1.f : 0.f, w1 = t == 1 ? 1.f : 0.f;
       bool use0 = t == 0, use1 = t == 1;
@@ -564,19 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         sync();
         if (!ok) break;
         tc_fence_after();
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int x = 0; x < 2 * REP; ++x) top = fmaxf(top, join[x * (kRows / REP) + qr].x);
-#pragma unroll
-        for (int x = 0; x < 2 * REP; ++x) {
-          const float2 a = join[x * (kRows / REP) + qr];
-          const float w = a.y == 0.f ? 0.f : a.x == -INFINITY ? 1.f : exp2f(a.x - top);
-          sum += w == 0.f ? 0.f : w * a.y;
-          if (x == r / (kRows / REP)) w0 = w;
-          if (x == REP + r / (kRows / REP)) w1 = w;
-        }
-        m = top;
-        l = sum;
+        const float2 a = join[r], b = join[kRows + r];
+        m = fmaxf(a.x, b.x);
+        w0 = a.y == 0.f ? 0.f : a.x == -INFINITY ? 1.f : exp2f(a.x - m);
+        w1 = b.y == 0.f ? 0.f : b.x == -INFINITY ? 1.f : exp2f(b.x - m);
+        l = (w0 == 0.f ? 0.f : w0 * a.y) + (w1 == 0.f ? 0.f : w1 * b.y);
         use0 = true;
         use1 = walk.n > 1;
         c0 = t * (D / 2);
@@ -597,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // values that are not finite, of the rows this token sees in this segment
           for (int j = 0; j < T; ++j) {
             if (!((odd[j >> 5] >> (j & 31)) & 1u)) continue;
-            if (parent ? !((tree.anc[i][j >> 5] >> (j & 31)) & 1u) : j > i) continue;
-            const uint2 y = *reinterpret_cast<const uint2*>(v + ((seq * n_kv + L + j) * Hkv + g) * D + c);
+            if (!sees(tree, parent != nullptr, i, j)) continue;
+            const uint2 y = *reinterpret_cast<const uint2*>(args.v + ((seq * n_kv + L + j) * Hkv + g) * D + c);
             if ((y.x & 0x7F80u) == 0x7F80u) x.x += bf16_lo(y.x);
             if ((y.x & 0x7F800000u) == 0x7F800000u) x.y += bf16_hi(y.x);
             if ((y.y & 0x7F80u) == 0x7F80u) x.z += bf16_lo(y.y);
@@ -608,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int64_t at = (seq * T + i) * H + g * G + (base + row - i * G);
-          *reinterpret_cast<uint2*>(o + at * D + c) =
+          *reinterpret_cast<uint2*>(args.o + at * D + c) =
               make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
         } else {
           work.part_o[(part * (D / 4) + c / 4) * (NT * kRows) + (NT == 2 ? t * kRows : 0) + row] = x;
@@ -626,64 +529,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (use1 && w1 != 0.f) ov[i] = fmaf(w1, __uint_as_float(x1[i]), ov[i]);
         }
       };
-      if constexpr (REP == 1) {
-        if (warp_rows) {
+      if (warp_rows) {
 #pragma unroll 1
-          for (int c = c0; c < c1; c += 16) {
-            float ov[16];
-            read16(c, ov);
-            if (qr < nr) {
+        for (int c = c0; c < c1; c += 16) {
+          float ov[16];
+          read16(c, ov);
+          if (r < nr) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4) put(qr, c + i, make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]), l);
-            }
+            for (int i = 0; i < 16; i += 4) put(r, c + i, make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]), l);
           }
         }
-      } else {
-        // The copies' shares are added through shared memory (the query rows' place, all scores are
-        // formed): kCols columns of each half a round.
-        constexpr int kCols = D / 4, kRowsOf = kRows / REP;
-        float4* buf = reinterpret_cast<float4*>(smem);  // [warp][kCols / 4][32]
-        float* sums = reinterpret_cast<float*>(join);   // the rows' sums, once everyone has read the parts
-        sync();
-        if (!ok) break;
-        if (t == 0 && r < kRowsOf) sums[r] = l;
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += kCols) {
-          if (warp_rows) {
-#pragma unroll 1
-            for (int x = 0; x < kCols; x += 16) {
-              float ov[16];
-              read16(c0 + c + x, ov);
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                buf[(warp * (kCols / 4) + (x + i) / 4) * 32 + lane] = make_float4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
-            }
-          }
-          sync();
-          if (!ok) break;
-          for (int e = tid; e < kRowsOf * 2 * (kCols / 4); e += kSoftmax) {
-            const int row = e % kRowsOf, c4 = e / kRowsOf % (kCols / 4), half = e / kRowsOf / (kCols / 4);
-            if (row >= nr) continue;
-            float4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int y = 0; y < REP; ++y) {
-              const int lanes_of = half * kRows + y * kRowsOf + row;  // lane of the row's copy y in that group
-              const float4 z = buf[(lanes_of / 32 * (kCols / 4) + c4) * 32 + lanes_of % 32];
-              x = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
-            }
-            put(row, half * (D / 2) + c + 4 * c4, x, sums[row]);
-          }
-          sync();
-          if (!ok) break;
-        }
-        if (!ok) break;
       }
       __syncwarp();
-      if (qr < nr && r == qr && (NT == 2 || t == 0)) {
+      if (r < nr && (NT == 2 || t == 0)) {
         if (!whole)
-          work.part_ml[part * (NT * kRows) + (NT == 2 ? t * kRows : 0) + qr] = make_float2(m, l);
-        else if (lse)
-          lse[(seq * T + slot_i) * H + g * G + (base + qr - slot_i * G)] =
+          work.part_ml[part * (NT * kRows) + (NT == 2 ? t * kRows : 0) + r] = make_float2(m, l);
+        else if (args.lse)
+          args.lse[(seq * T + slot_i) * H + g * G + (base + r - slot_i * G)] =
               l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
     }
@@ -870,30 +732,25 @@ Layout layout(const Shape& s, bool with_weight) {
   return L;
 }
 
-template <int D, int NT, int REP>
-cudaError_t launch(const Shape& s, const void* q, const void* k, const void* v, const int32_t* kv_len,
-                   const int32_t* parent, void* o, float* lse, float* scores, int64_t score_stride, Work work,
-                   int32_t* status, cudaStream_t st) {
-  using C = Cfg<D, NT>;
+template <int D, int NT>
+cudaError_t launch(const Shape& s, const void* k, const void* v, const TreeArgs& a, int ctas, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!map_cache_rows(&mk, k, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows) ||
       !map_cache_rows(&mv, v, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows))
     return cudaErrorNotSupported;
-  cudaError_t e = ensure_smem((const void*)tree_attn_kernel<D, NT, REP>, C::kSmem);
+  const cudaError_t e = ensure_smem((const void*)tree_attn_kernel<D, NT>, Cfg<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
-  const int R = (int)s.n_q * (s.H / s.Hkv), np = (R + NT * kRows - 1) / (NT * kRows);
-  const int64_t items = (int64_t)s.batch * s.Hkv * np, most = items * ((s.n_kv + kRows - 1) / kRows);
-  const int ctas = (int)(most < kMaxCtas ? most : kMaxCtas);
-  e = launch_after(tree_attn_kernel<D, NT, REP>, dim3((unsigned)ctas), kThreads, st, C::kSmem, mk, mv,
-                   static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(v), kv_len, parent,
-                   static_cast<uint16_t*>(o), lse, scores, score_stride, work, status, s.batch, (int)s.n_q, s.n_kv, s.H,
-                   s.Hkv, s.scale * kLog2e);
-  if (e != cudaSuccess) return e;
+  return launch_after(tree_attn_kernel<D, NT>, dim3((unsigned)ctas), kThreads, st, Cfg<D, NT>::kSmem, mk, mv, a);
+}
+
+template <int D>
+cudaError_t launch_merge(const Shape& s, const TreeArgs& a, int tile_rows, int ctas, cudaStream_t st) {
+  const int R = a.T * (a.H / a.Hkv);
   int lanes = 1;  // lanes for rows
   while (lanes < 32 && lanes < R) lanes *= 2;
   return launch_after(tree_attn_merge_kernel<D>, dim3((unsigned)(s.Hkv * ((R + lanes - 1) / lanes)), (unsigned)s.batch),
-                      32 * (D / 16) * kSplits, st, 0, work, static_cast<uint16_t*>(o), lse, s.batch, (int)s.n_q, s.H, s.Hkv,
-                      NT * kRows, lanes, ctas);
+                      32 * (D / 16) * kSplits, st, 0, a.work, a.o, a.lse, s.batch, a.T, a.H, a.Hkv, tile_rows, lanes,
+                      ctas);
 }
 
 }  // namespace
@@ -905,23 +762,43 @@ cudaError_t launch_tree_attn(const Shape& s, const void* q, const void* k, const
                              cudaStream_t st) {
   const Layout L = layout(s, weight != nullptr);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const Work work = {reinterpret_cast<int64_t*>(w + L.prefix), reinterpret_cast<float4*>(w + L.part_o),
-                     reinterpret_cast<float2*>(w + L.part_ml)};
-  if (weight && !lse) lse = reinterpret_cast<float*>(w + L.lse);
-  const int64_t R = s.n_q * (s.H / s.Hkv);
-  const auto pick = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    return R <= 32 ? launch<D, 1, 4> : R <= 64 ? launch<D, 1, 2> : R <= kRows ? launch<D, 1, 1> : launch<D, 2, 1>;
-  };
-  const auto run = s.d == 64 ? pick(std::integral_constant<int, 64>()) : pick(std::integral_constant<int, 128>());
   const bool kept = weight && keeps_scores(s);
-  float* scores = kept ? reinterpret_cast<float*>(w + L.weight) : nullptr;
-  const cudaError_t e = run(s, q, k, v, kv_len, parent, o, lse, scores, score_stride(s), work, status, st);
+  TreeArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.v = static_cast<const uint16_t*>(v);
+  a.kv_len = kv_len;
+  a.parent = parent;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = weight && !lse ? reinterpret_cast<float*>(w + L.lse) : lse;
+  a.scores = kept ? reinterpret_cast<float*>(w + L.weight) : nullptr;
+  a.score_stride = score_stride(s);
+  a.work = {reinterpret_cast<int64_t*>(w + L.prefix), reinterpret_cast<float4*>(w + L.part_o),
+            reinterpret_cast<float2*>(w + L.part_ml)};
+  a.status = status;
+  a.batch = s.batch;
+  a.T = (int)s.n_q;
+  a.n_kv = s.n_kv;
+  a.H = s.H;
+  a.Hkv = s.Hkv;
+  a.qscale = s.scale * kLog2e;
+  const int R = a.T * (s.H / s.Hkv), nt = row_tiles(s);
+  int tile_rows = nt * kRows;
+  const int64_t most = (int64_t)s.batch * s.Hkv * ((R + tile_rows - 1) / tile_rows) * ((s.n_kv + kRows - 1) / kRows);
+  const int ctas = (int)(most < kMaxCtas ? most : kMaxCtas);
+  cudaError_t e;
+  if (R <= kFewRows)
+    e = launch_tree_attn_few(s, k, v, a, ctas, &tile_rows, st);
+  else if (s.d == 64)
+    e = nt == 1 ? launch<64, 1>(s, k, v, a, ctas, st) : launch<64, 2>(s, k, v, a, ctas, st);
+  else
+    e = nt == 1 ? launch<128, 1>(s, k, v, a, ctas, st) : launch<128, 2>(s, k, v, a, ctas, st);
+  if (e == cudaSuccess)
+    e = s.d == 64 ? launch_merge<64>(s, a, tile_rows, ctas, st) : launch_merge<128>(s, a, tile_rows, ctas, st);
   if (e != cudaSuccess || !weight) return e;
-  if (!kept) return launch_cache_weight(s, q, k, kv_len, parent, nullptr, lse, weight, nullptr, w + L.weight, st);
+  if (!kept) return launch_cache_weight(s, q, k, kv_len, parent, nullptr, a.lse, weight, nullptr, w + L.weight, st);
   const int64_t per = 4 * kWeighThreads;
   return launch_after(tree_attn_weigh_kernel, dim3((unsigned)((s.n_kv + per - 1) / per), (unsigned)s.batch),
-                      kWeighThreads, st, 0, scores, score_stride(s), lse, kv_len, weight, (int)s.n_q, s.n_kv, s.H, s.Hkv);
+                      kWeighThreads, st, 0, a.scores, a.score_stride, a.lse, kv_len, weight, a.T, s.n_kv, s.H, s.Hkv);
 }
 
 }  // namespace hisa
