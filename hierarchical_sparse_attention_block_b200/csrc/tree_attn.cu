@@ -16,8 +16,8 @@
 // SM.  An item that one CTA holds whole is written by it; the others leave (max, sum, unnormalised
 // output) per range in the workspace, merged by tree_attn_merge_kernel.
 //
-// This file's kernel takes 65 query rows and more of a KV head, one or two tiles of 128 rows at a time;
-// tree_attn_few.cu up to 64, with the keys as the product's rows.
+// This file's kernel takes 17 query rows and more of a KV head, one or two tiles of 128 rows at a time;
+// tree_attn_few.cu up to 16, with the keys as the product's rows.
 //
 // Roles of a CTA: two softmax groups of four warps, one thread per query row (TMEM lane = row); then
 // one thread each for the K loads (TMA), the MMAs (tcgen05) and the V loads.  Two row tiles: each
@@ -708,9 +708,10 @@ __global__ void __launch_bounds__(kWeighThreads)
 
 int row_tiles(const Shape& s) { return s.n_q * (s.H / s.Hkv) > kRows ? 2 : 1; }
 
-// The weights come from kept scores while writing and reading those (8 bytes a query row and key) moves
-// less than reading K again (2 d bytes a KV head and key).
-bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) * 4 <= s.d; }
+// With few query rows the weights come from kept scores: writing and reading those moves 8 bytes a query
+// row and key, reading K again 2 d bytes a KV head and key (8 x 64K rows, one query row a KV head: 500 us
+// this way, 740 with K read again).
+bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kFewRows; }
 int64_t score_stride(const Shape& s) { return (s.n_kv + kRows - 1) / kRows * kRows; }
 
 struct Layout {
@@ -781,13 +782,12 @@ cudaError_t launch_tree_attn(const Shape& s, const void* q, const void* k, const
   a.H = s.H;
   a.Hkv = s.Hkv;
   a.qscale = s.scale * kLog2e;
-  const int R = a.T * (s.H / s.Hkv), nt = row_tiles(s);
-  int tile_rows = nt * kRows;
+  const int R = a.T * (s.H / s.Hkv), nt = row_tiles(s), tile_rows = R <= kFewRows ? kFewRows : nt * kRows;
   const int64_t most = (int64_t)s.batch * s.Hkv * ((R + tile_rows - 1) / tile_rows) * ((s.n_kv + kRows - 1) / kRows);
   const int ctas = (int)(most < kMaxCtas ? most : kMaxCtas);
   cudaError_t e;
   if (R <= kFewRows)
-    e = launch_tree_attn_few(s, k, v, a, ctas, &tile_rows, st);
+    e = launch_tree_attn_few(s, k, v, a, ctas, st);
   else if (s.d == 64)
     e = nt == 1 ? launch<64, 1>(s, k, v, a, ctas, st) : launch<64, 2>(s, k, v, a, ctas, st);
   else

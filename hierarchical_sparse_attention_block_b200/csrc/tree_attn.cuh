@@ -94,9 +94,9 @@ __device__ __forceinline__ void prefetch_next(Walk walk, const TreeArgs& a, int 
   if (a.parent && r * 32 < a.T) prefetch_l2(a.parent + (int64_t)walk.s * a.T + r * 32);
 }
 
-// Up to 64 query rows per KV head (tree_attn_few.cu).  *tile_rows: rows of an item in the partial results.
-constexpr int kFewRows = 64;
+// Up to kFewRows query rows per KV head (tree_attn_few.cu), which are also an item's rows in the partial results.
+constexpr int kFewRows = 16;
 cudaError_t launch_tree_attn_few(const Shape& s, const void* k, const void* v, const TreeArgs& a, int ctas,
-                                 int* tile_rows, cudaStream_t st);
+                                 cudaStream_t st);
 
 }  // namespace hisa

@@ -1,13 +1,15 @@
-// hisa_tree_attn_fwd for up to 64 query rows per KV head (a plain decode step, small trees), on the
+// hisa_tree_attn_fwd for up to 16 query rows per KV head (a plain decode step, small trees), on the
 // 5th-generation tensor cores with the keys as the product's rows:
 //
-//   S^T = K Q^T  (128 keys x N),   O^T += V^T P^T  (D x N),   N = 16, 32 or 64 >= T H / Hk query rows.
+//   S^T = K Q^T  (128 keys x N),   O^T += V^T P^T  (D x N),   N = 16 >= T H / Hk query rows.
 //
-// The call is bound by the cache's bytes (K and V once).  With the query rows as the M = 128 of the
-// products, as tree_attn.cu has them, one to 64 of 128 rows would be padding, and their products cost
-// enough power to lower the clocks: 8 x 64K rows, one query row: 580 us that way.  Here the products
-// shrink with N, and a thread, which owns a key, forms that key's weights of all N rows: every
-// exponential is one that counts.
+// The call is bound by the cache's bytes (K and V once): 8 x 64K rows, one query row a KV head, take
+// 432 us, 6.7 TB/s.  With the query rows as the M = 128 of the products, as tree_attn.cu has them, one to
+// 16 of 128 rows would be padding (446 us, with weights of 8 bits).  Here the products shrink with N, a
+// thread, which owns a key, forms that key's weights of all rows, and keeping the scores for the weights
+// that the rows receive is a coalesced store.  From 17 rows on the stores of the weights, two bytes at a
+// time, take longer than the tile's bytes (8 x 32K rows, 32 query rows: 150 us this way with N = 32, 129
+// the other).
 //
 // Work and ring buffers are those of tree_attn.cu (one row tile).  Scores and weights have two buffers,
 // used by the key tiles in turn; the two softmax groups of four warps take half of the query rows each.
@@ -32,13 +34,15 @@ constexpr int kThreads = kSoftmax + 96;
 constexpr int kWarpK = 8, kWarpMMA = 9, kWarpV = 10;
 constexpr uint32_t kTmemCols = 256;  // score buffer b at 64 b, the output at 128
 
-template <int D, int N>
+constexpr int N = kFewRows;
+
+template <int D>
 struct Cfg {
   static constexpr int kTile = kHalf * (D / 64);   // a K or V tile
   static constexpr int kQHalf = N * 128;           // 64 columns of the query rows
   static constexpr int kWeights = N * 256;         // one part (high, low) of a tile's weights: N rows x 128 keys
   // ring slots of K and of V: what 227 KB hold beside the rest
-  static constexpr int KS = D == 64 ? (N == 64 ? 4 : 6) : N == 64 ? 2 : 3, VS = D == 64 ? (N == 64 ? 4 : 5) : N == 16 ? 3 : 2;
+  static constexpr int KS = D == 64 ? 6 : 3, VS = D == 64 ? 6 : 3;
   // V before the weights and the rest: with D = 64 the second product's upper 64 rows, which nobody
   // reads, come from the 16 KB behind a V tile
   static constexpr int K_OFF = 0, V_OFF = K_OFF + KS * kTile, P_OFF = V_OFF + VS * kTile;
@@ -73,11 +77,11 @@ struct Cfg {
   static_assert(P_OFF - V_OFF >= kTile && 4 * kWeights >= kHalf, "what lies behind a V tile is this block's memory");
 };
 
-template <int D, int N>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ TreeArgs args) {
-  using C = Cfg<D, N>;
+  using C = Cfg<D>;
   const int32_t* const parent = args.parent;
   int32_t* const status = args.status;
   const int T = args.T, H = args.H, Hkv = args.Hkv, G = H / Hkv, R = T * G;
@@ -303,56 +307,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         // the rows' scores of this key, -inf where a row does not see it
-        constexpr int CB = NR < 16 ? NR : 16;
-        auto load = [&](int c, uint32_t(&s)[CB]) {
+        auto load = [&](uint32_t(&s)[NR]) {
           __syncwarp();
-          tmem_ld<CB>(ts + (uint32_t)c, s);
+          tmem_ld<NR>(ts, s);
           if (tail && j >= 0) {
 #pragma unroll
-            for (int i = 0; i < CB; ++i)
-              if (j >= T || !sees(tree, parent != nullptr, slots[row0 + c + i], j)) s[i] = 0xFF800000u;
+            for (int i = 0; i < NR; ++i)
+              if (j >= T || !sees(tree, parent != nullptr, slots[row0 + i], j)) s[i] = 0xFF800000u;
           }
         };
         float p[NR];
         while (true) {
           bool up = false;
+          uint32_t s[NR];
+          load(s);
+          if (args.scores) {
 #pragma unroll
-          for (int c = 0; c < NR; c += CB) {
-            uint32_t s[CB];
-            load(c, s);
-            if (args.scores) {
+            for (int i = 0; i < NR; ++i)
+              if (row0 + i < R)
+                args.scores[((seq * Hkv + g) * R + row0 + i) * args.score_stride + t0 + r] = __uint_as_float(s[i]) * qscale;
+          }
 #pragma unroll
-              for (int i = 0; i < CB; ++i)
-                if (row0 + c + i < R)
-                  args.scores[((seq * Hkv + g) * R + row0 + c + i) * args.score_stride + t0 + r] =
-                      __uint_as_float(s[i]) * qscale;
-            }
-#pragma unroll
-            for (int i = 0; i < CB; i += 2) {
-              const float4 st = *reinterpret_cast<const float4*>(rows + c + i);
-              const float x0 = fmaf(__uint_as_float(s[i]), qscale, -st.x), x1 = fmaf(__uint_as_float(s[i + 1]), qscale, -st.z);
-              up |= x0 > st.y;
-              up |= x1 > st.w;
-              p[c + i] = fast_exp2(x0);  // 0 where masked
-              p[c + i + 1] = fast_exp2(x1);
-            }
+          for (int i = 0; i < NR; i += 2) {
+            const float4 st = *reinterpret_cast<const float4*>(rows + i);
+            const float x0 = fmaf(__uint_as_float(s[i]), qscale, -st.x), x1 = fmaf(__uint_as_float(s[i + 1]), qscale, -st.z);
+            up |= x0 > st.y;
+            up |= x1 > st.w;
+            p[i] = fast_exp2(x0);  // 0 where masked
+            p[i + 1] = fast_exp2(x1);
           }
           if (__any_sync(0xFFFFFFFFu, up) && lane == 0) raise_flag[t] = 1;
           agree();
           if (!ok || !raise_flag[t]) break;
           // the rows' max over the tile, per warp and then over the warps
+          float mine = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NR; c += CB) {
-            uint32_t s[CB];
-            load(c, s);
-            float mine = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < CB; ++i) {
-              const float top = warp_max(__uint_as_float(s[i]) * qscale);
-              if (lane == i) mine = top;
-            }
-            if (lane < CB) per_warp[(warp & 3) * N + c + lane] = mine;
+          for (int i = 0; i < NR; ++i) {
+            const float top = warp_max(__uint_as_float(s[i]) * qscale);
+            if (lane == i) mine = top;
           }
+          if (lane < NR) per_warp[(warp & 3) * N + lane] = mine;
           agree();
           if (!ok) break;
           if (r == 0) raise_flag[t] = 0;
@@ -376,15 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + (buf ^ 1)), (uint32_t)((cnt - 1) >> 1) & 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < NR; c += 8) {
-              uint32_t ov[8];
-              __syncwarp();
-              tmem_ld<8>(to + (uint32_t)c, ov);
+            uint32_t ov[NR];
+            __syncwarp();
+            tmem_ld<NR>(to, ov);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alphas[c + i]);
-              tmem_st<8>(to + (uint32_t)c, ov);
-            }
+            for (int i = 0; i < NR; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alphas[i]);
+            tmem_st<NR>(to, ov);
           }
         }
         if (!ok) break;
@@ -422,16 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       // the rows' sums: over the lanes, then over the warps
+      float mine = 0.f;
 #pragma unroll
-      for (int c = 0; c < NR; c += 8) {
-        float mine = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float sum = warp_sum(l[c + i]);
-          if (lane == i) mine = sum;
-        }
-        if (lane < 8) per_warp[(warp & 3) * N + c + lane] = mine;
+      for (int i = 0; i < NR; ++i) {
+        const float sum = warp_sum(l[i]);
+        if (lane == i) mine = sum;
       }
+      if (lane < NR) per_warp[(warp & 3) * N + lane] = mine;
       agree();
       if (!ok) break;
       if (r < NR) {
@@ -451,17 +439,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t part = (int64_t)blockIdx.x * 2 + walk.slot();
       const uint32_t any_odd = odd[0] | odd[1] | odd[2] | odd[3] | odd[4] | odd[5] | odd[6] | odd[7];
       // Output: thread = column.
-#pragma unroll 1
-      for (int c = 0; c < NR && row0 + c < R; c += 8) {
-        uint32_t ov[8];
-        __syncwarp();
-        tmem_ld<8>(to + (uint32_t)c, ov);
-        if (r >= D) continue;
+      uint32_t ov[NR];
+      __syncwarp();
+      tmem_ld<NR>(to, ov);
+      if (r < D) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = row0 + c + i;
+        for (int i = 0; i < NR; ++i) {
+          const int row = row0 + i;
           if (row >= R) continue;
-          const float sum = join[c + i].y;
+          const float sum = join[i].y;
           float y = sum == 0.f ? 0.f : __uint_as_float(ov[i]);
           const int slot = slots[row];
           if (any_odd && !(treed && tree.end[slot] != kRoot)) {
@@ -473,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (whole) {
-            const int64_t at = (seq * T + slot) * H + g * G + (row - slot * G);
-            reinterpret_cast<__nv_bfloat16*>(args.o)[at * D + r] = __float2bfloat16_rn(sum == 0.f ? y : y / sum);
+            const int64_t to_row = (seq * T + slot) * H + g * G + (row - slot * G);
+            reinterpret_cast<__nv_bfloat16*>(args.o)[to_row * D + r] = __float2bfloat16_rn(sum == 0.f ? y : y / sum);
           } else {
             reinterpret_cast<float*>(args.work.part_o + (part * (D / 4) + r / 4) * N + row)[r & 3] = y;
           }
@@ -502,28 +488,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, int N>
+template <int D>
 cudaError_t launch(const Shape& s, const void* k, const void* v, const TreeArgs& a, int ctas, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!map_cache_rows(&mk, k, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows) ||
       !map_cache_rows(&mv, v, D, (uint64_t)s.Hkv, (uint64_t)s.n_kv, (uint64_t)s.batch, kRows))
     return cudaErrorNotSupported;
-  const cudaError_t e = ensure_smem((const void*)tree_attn_few_kernel<D, N>, Cfg<D, N>::kSmem);
+  const cudaError_t e = ensure_smem((const void*)tree_attn_few_kernel<D>, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_after(tree_attn_few_kernel<D, N>, dim3((unsigned)ctas), kThreads, st, Cfg<D, N>::kSmem, mk, mv, a);
+  return launch_after(tree_attn_few_kernel<D>, dim3((unsigned)ctas), kThreads, st, Cfg<D>::kSmem, mk, mv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_attn_few(const Shape& s, const void* k, const void* v, const TreeArgs& a, int ctas,
-                                 int* tile_rows, cudaStream_t st) {
-  const int R = a.T * (a.H / a.Hkv);
-  *tile_rows = R <= 16 ? 16 : R <= 32 ? 32 : kFewRows;
-  if (s.d == 64)
-    return R <= 16 ? launch<64, 16>(s, k, v, a, ctas, st) : R <= 32 ? launch<64, 32>(s, k, v, a, ctas, st)
-                                                                     : launch<64, 64>(s, k, v, a, ctas, st);
-  return R <= 16 ? launch<128, 16>(s, k, v, a, ctas, st) : R <= 32 ? launch<128, 32>(s, k, v, a, ctas, st)
-                                                                    : launch<128, 64>(s, k, v, a, ctas, st);
+                                 cudaStream_t st) {
+  return s.d == 64 ? launch<64>(s, k, v, a, ctas, st) : launch<128>(s, k, v, a, ctas, st);
 }
 
 }  // namespace hisa

@@ -348,7 +348,7 @@ hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_
  *   o[s][i][h]   = sum_{t in V(i)} softmax_t(z(t)) v[s][t][g]
  *   lse[s][i][h] = ln sum_{t in V(i)} exp(z(t))       (lse nullable)
  * An empty slot gives o = 0, lse = -inf.  fp32 scores, sums and accumulation,
- * bf16 output; with up to 64 query rows per KV head (T * H / Hk) the weights
+ * bf16 output; with up to 16 query rows per KV head (T * H / Hk) the weights
  * multiply V to 16 significant bits, with more as bf16 (each output then stays
  * within 2^-8 sum_t softmax_t |v| of the exact one before its own rounding).
  * weight (nullable) [b][n_kv] fp32: the attention weight each row receives,

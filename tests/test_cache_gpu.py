@@ -5,7 +5,7 @@ the tensor cores truncate), and its scaling, the exponential and the sums add a 
 the product as a pair of bf16 numbers is off by 2^-16 more.  So a softmax weight is off by a relative
 delta = (d + 8) 2^-23 size + 2^-14 at most, numerator and denominator each, and
     |o - ref|   <= 2^-8 |ref| + (2 delta + e) sum p |v|      (2^-8: the output's rounding to bf16)
-with e = 2^-8 where a KV head has more than 64 query rows (T H / Hk): there a weight enters the product as one bf16
+with e = 2^-8 where a KV head has more than 16 query rows (T H / Hk): there a weight enters the product as one bf16
 number, off by half a step of 8 significant bits, 2^-8 relative, in the numerator alone; else e = 0.
     |lse - ref| <= delta + 2^-22 |ref|
     |w - ref|   <= (delta + 2^-21 max |lse|) received + 2^-20 |ref| + 2^-110
@@ -99,7 +99,7 @@ def check_tree(hs, x, H, Hk, d, weigh):
                                                         1 / math.sqrt(d))
     dl = delta(d, size)
     close(lse, rl, dl + 2.0**-22 * rl.abs().nan_to_num(0, 0, 0), "lse")
-    e = 2.0**-8 if T * H // Hk > 64 else 0.0
+    e = 2.0**-8 if T * H // Hk > 16 else 0.0
     close(o, ro, 2.0**-8 * ro.abs() + (2 * dl + e) * spread, "o")
     top = float(rl[rl > -math.inf].abs().max()) if (rl > -math.inf).any() else 0.0
     if weigh:
@@ -572,7 +572,7 @@ def test_a_bounded_cache_through_a_decode(hs):
         o, lse = hs.tree_attn(p, q.cuda(), g["k"], g["v"], kv_len, parent=parent.cuda())
         counted = [set(int(i) for i in row if i >= 0) for row in path]
         ro, rl, received, spread, size = ref.tree_attention(q, k, v, lens, parent, scale, counted)
-        close(o, ro, 2.0**-8 * ro.abs() + 2 * delta(d, size) * spread, "o")
+        close(o, ro, 2.0**-8 * ro.abs() + (2 * delta(d, size) + 2.0**-8) * spread, "o")
         hs.hisa_cache_weight(p, q.cuda(), g["k"], kv_len, lse, g["weight"], parent=parent.cuda(), path=path.cuda())
         weight = ref.weight_after(weight, received, lens, T).float()
         rows = torch.where(path >= 0, path + lens[:, None], -1)
