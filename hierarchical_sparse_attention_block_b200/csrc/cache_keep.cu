@@ -2,14 +2,17 @@
 //
 // Between the first n_first and the last n_recent rows, the K = budget - n_first - n_recent rows
 // with the largest weight (ties: the lower row) are kept: an exact selection of the K-th largest key
-// by radix, 8 bits a pass from the top, then one counting and one emitting sweep in row order.
+// by radix, 8 bits a pass from the top, and a sweep that emits the taken rows in order.
 //
 // A cluster of up to 16 CTAs takes one sequence, a contiguous part of its rows each, so that a single
-// long cache is not left to one SM; the first 47K rows of a part stay in shared memory, each sweep reads
-// the others again (L2).  A pass counts into 32 copies of the 256 counters, copy =
-// lane: the atomics of a warp never meet, whatever the weights' distribution (accumulated weights
-// share few exponents, equal ones are frequent).  The CTAs exchange their 256 sums through
-// distributed shared memory.  The bound is the sweeps' latency, not the 4 bytes a row.
+// long cache is not left to one SM; the first 46K keys of a part stay in shared memory, each sweep
+// reads the others again (L2).  A pass counts into 32 copies of the 256 counters, copy = lane: the
+// atomics of a warp never meet, whatever the weights' distribution (accumulated weights share few
+// exponents, equal ones are frequent).  The CTAs exchange their 256 sums through distributed shared
+// memory.  Two passes fix 16 bits of the threshold; where few keys share them (the usual case), one
+// more sweep counts the keys above and collects those few, and the last two passes and the split of
+// the ties work on them alone; else they are sweeps too.  Keys are read four at a time: the bound is
+// the number of instructions a key and the cluster's barriers, not the 4 bytes a row.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -21,40 +24,45 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kUnroll = 16;  // keys a thread reads at once
 constexpr int kMaxCluster = 16;
-constexpr int kStaged = 47 * 1024;  // rows a CTA holds in shared memory
+constexpr int kStaged = 46 * 1024;  // keys a CTA holds in shared memory
+constexpr int kFew = 1024;          // keys of the cluster that are collected
 
-struct Shared {
+struct alignas(16) Shared {
   uint32_t copies[256][32];  // counters of the running pass, copy = lane
   uint32_t sums[2][256];     // this CTA's sums, of the passes in turn (read by the whole cluster)
   uint32_t totals[256];      // the cluster's
   uint32_t counts[2];        // this CTA's keys above and at the threshold
   uint32_t warp_gt[kWarps], warp_eq[kWarps];
   uint32_t digit, above, at;
+  uint32_t n_few;             // collected keys of this CTA
+  uint32_t few_key[kFew];
+  uint16_t few_warp[kFew];    // the warp whose range the key lies in
 };
-
 static_assert(sizeof(Shared) + 4 * kStaged <= 227 * 1024, "shared memory budget");
 
-// Order-preserving key of a weight: every NaN above +inf.
+// Order-preserving key of a weight: every NaN above +inf.  No weight's key is 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(__fadd_rn(w, 0.0f));  // -0 + 0 = +0
-  return u ^ ((u & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return w != w ? 0xFFFFFFFFu : k;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     cache_keep_kernel(const float* __restrict__ weight, const int32_t* kv_len, int64_t n_kv, int budget, int n_first,
                       int n_recent, int32_t* __restrict__ keep_idx, int32_t* kept_len, int32_t* __restrict__ status) {
-  extern __shared__ uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   Shared& sm = *reinterpret_cast<Shared*>(smem);
-  uint32_t* held = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
+  uint4* held = reinterpret_cast<uint4*>(smem + sizeof(Shared));
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t seq = blockIdx.x / nc;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* out = keep_idx + seq * budget;
   int64_t L = kv_len[seq];
+  for (int i = tid; i < 256 * 32 / 4; i += kThreads) reinterpret_cast<uint4*>(sm.copies)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) sm.n_few = 0;
+  if (tid < kWarps) sm.warp_gt[tid] = sm.warp_eq[tid] = 0;
   cluster.sync();  // kept_len may be kv_len
   if (L < 0 || L > n_kv) {
     if (rank == 0 && tid == 0 && status) atomicOr(status, kStatusBadIndex);
@@ -74,57 +82,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int K = budget - n_first - n_recent;
   if (K == 0) return;
 
-  // This CTA's part [b0, b0 + n) of the rows between.
-  const int64_t all = L - n_first - n_recent;
-  const int64_t b0 = all * rank / nc;
-  const int n = (int)(all * (rank + 1) / nc - b0);
-  const float* w = weight + seq * n_kv + n_first + b0;
-  const int staged = min(n, kStaged);  // the first rows' keys stay here
-  auto key = [&](int i) { return i < staged ? held[i] : weight_key(w[i]); };
+  // The rows between, in groups of four from a 16-byte boundary at or before the first; this CTA has the
+  // groups [0, n) of its part.  Rows outside the range get key 0, which is never taken.
+  const float* row = weight + seq * n_kv;
+  const int lead = (int)((reinterpret_cast<uintptr_t>(row + n_first) >> 2) & 3);
+  const int64_t begin = n_first - lead, end = L - n_recent;
+  const int64_t groups = (end - begin + 3) / 4, g0 = groups * rank / nc;
+  const int n = (int)(groups * (rank + 1) / nc - g0);
+  const int64_t t0 = begin + 4 * g0;  // row of the part's first key
+  const int staged = min(n, kStaged / 4);
+  auto fetch = [&](int q) {  // keys of group q
+    const int64_t t = t0 + 4 * (int64_t)q;
+    if (t >= n_first && t + 4 <= end) {
+      const float4 w = *reinterpret_cast<const float4*>(row + t);
+      return make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
+    }
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = t + i >= n_first && t + i < end ? weight_key(row[t + i]) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
+  auto keys = [&](int q) { return q < staged ? held[q] : fetch(q); };
+  // Every warp has a contiguous range of groups in the sweeps that keep the order.
+  const int span = ((n + kWarps - 1) / kWarps + 31) & ~31;
+  const int q0 = min(warp * span, n), q1 = min(q0 + span, n);
 
   uint32_t prefix = 0, mask = 0, krem = (uint32_t)K;
-  bool tie = true;  // of the keys equal to the prefix under the mask the first krem are taken, else all
+  bool tie = true;   // of the keys equal to the prefix under the mask the first krem are taken, else all
+  bool few = false;  // the keys that match 16 bits of the threshold are collected
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    for (int i = tid; i < 256 * 32; i += kThreads) (&sm.copies[0][0])[i] = 0;
-    __syncthreads();
+    auto count = [&](uint32_t k) {
+      if ((k & mask) == prefix) atomicAdd(&sm.copies[(k >> shift) & 255u][lane], 1u);
+    };
     if (pass == 0) {
-      for (int i0 = 0; i0 < n; i0 += kUnroll * kThreads) {
-        float x[kUnroll];
+      for (int c0 = 0; c0 < n; c0 += 4 * kThreads) {
+        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = i0 + u * kThreads + tid;
-          x[u] = i < n ? w[i] : 0.f;
+        for (int u = 0; u < 4; ++u) {
+          const int q = c0 + u * kThreads + tid;
+          if (q < n) x[u] = fetch(q);
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = i0 + u * kThreads + tid;
-          if (i >= n) continue;
-          const uint32_t k = weight_key(x[u]);
-          if (i < staged) held[i] = k;
-          atomicAdd(&sm.copies[k >> 24][lane], 1u);
+        for (int u = 0; u < 4; ++u) {
+          const int q = c0 + u * kThreads + tid;
+          if (q >= n) continue;
+          if (q < staged) held[q] = x[u];
+          atomicAdd(&sm.copies[x[u].x >> 24][lane], 1u);
+          atomicAdd(&sm.copies[x[u].y >> 24][lane], 1u);
+          atomicAdd(&sm.copies[x[u].z >> 24][lane], 1u);
+          atomicAdd(&sm.copies[x[u].w >> 24][lane], 1u);
         }
       }
+    } else if (few) {
+      for (int i = tid; i < (int)sm.n_few; i += kThreads) count(sm.few_key[i]);
     } else {
-      for (int i0 = 0; i0 < n; i0 += kUnroll * kThreads) {
-        uint32_t x[kUnroll];
+      for (int c0 = 0; c0 < n; c0 += 4 * kThreads) {
+        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = i0 + u * kThreads + tid;
-          x[u] = i < n ? key(i) : ~prefix;
+        for (int u = 0; u < 4; ++u) {
+          const int q = c0 + u * kThreads + tid;
+          x[u] = q < n ? keys(q) : make_uint4(0u, 0u, 0u, 0u);  // (0 may match only where no key is taken)
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-          if ((x[u] & mask) == prefix) atomicAdd(&sm.copies[(x[u] >> shift) & 255u][lane], 1u);
+        for (int u = 0; u < 4; ++u) {
+          count(x[u].x);
+          count(x[u].y);
+          count(x[u].z);
+          count(x[u].w);
+        }
       }
     }
     __syncthreads();
-    // the copies' sums: a warp takes 8 counters, its lanes their copies
+    // the copies' sums: a warp takes 8 counters, its lanes their copies, which are then free again
     uint32_t* mine = sm.sums[pass & 1];
 #pragma unroll
     for (int b = 0; b < 256 / kWarps; ++b) {
       const int bin = warp * (256 / kWarps) + b;
       const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, sm.copies[bin][lane]);
+      sm.copies[bin][lane] = 0;
       if (lane == 0) mine[bin] = c;
     }
     cluster.sync();
@@ -171,31 +207,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       tie = false;
       break;
     }
+    if (pass == 1 && sm.at <= kFew) {
+      // few keys share the 16 bits: count what lies above, collect them
+      few = true;
+      uint32_t gt = 0;
+      for (int c0 = q0; c0 < q1; c0 += 128) {
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = c0 + 32 * u + lane;
+          x[u] = q < q1 ? keys(q) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t k[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            gt += (k[i] & mask) > prefix;
+            if ((k[i] & mask) == prefix && k[i] != 0u) {
+              const uint32_t p = atomicAdd(&sm.n_few, 1u);
+              sm.few_key[p] = k[i];
+              sm.few_warp[p] = (uint16_t)warp;
+            }
+          }
+        }
+      }
+      gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+      if (lane == 0) sm.warp_gt[warp] = gt;
+      __syncthreads();
+    }
   }
 
-  // Every warp counts, then emits, a contiguous range of the part.
-  const int span = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(warp * span, n), w1 = min(w0 + span, n);
-  uint32_t gt = 0, eq = 0;
-  for (int c0 = w0; c0 < w1; c0 += 256) {
-    uint32_t x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = c0 + 32 * u + lane;
-      x[u] = i < w1 ? key(i) : 0u;
+  // What every warp's range holds above and at the threshold.
+  if (few) {
+    for (int i = tid; i < (int)sm.n_few; i += kThreads) {
+      const uint32_t k = sm.few_key[i] & mask;
+      if (k > prefix) atomicAdd(&sm.warp_gt[sm.few_warp[i]], 1u);
+      if (k == prefix) atomicAdd(&sm.warp_eq[sm.few_warp[i]], 1u);
     }
+  } else {
+    uint32_t gt = 0, eq = 0;
+    for (int c0 = q0; c0 < q1; c0 += 128) {
+      uint4 x[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const bool in = c0 + 32 * u + lane < w1;
-      gt += in && (x[u] & mask) > prefix;
-      eq += in && (x[u] & mask) == prefix;
+      for (int u = 0; u < 4; ++u) {
+        const int q = c0 + 32 * u + lane;
+        x[u] = q < q1 ? keys(q) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t k[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gt += (k[i] & mask) > prefix;
+          eq += (k[i] & mask) == prefix && k[i] != 0u;
+        }
+      }
     }
-  }
-  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  if (lane == 0) {
-    sm.warp_gt[warp] = gt;
-    sm.warp_eq[warp] = eq;
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    if (lane == 0) {
+      sm.warp_gt[warp] = gt;
+      sm.warp_eq[warp] = eq;
+    }
   }
   __syncthreads();
   if (warp == 0) {
@@ -222,24 +296,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t quota = tie ? krem : 0xFFFFFFFFu;
   uint32_t place = n_first + above + min(ties, quota);
   const uint32_t below = (1u << lane) - 1u;
-  const int32_t row0 = (int32_t)(n_first + b0);
-  for (int c0 = w0; c0 < w1; c0 += 256) {
-    uint32_t x[8];
+  for (int c0 = q0; c0 < q1; c0 += 64) {
+    uint4 x[2];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = c0 + 32 * u + lane;
-      x[u] = i < w1 ? key(i) : 0u;
+    for (int u = 0; u < 2; ++u) {
+      const int q = c0 + 32 * u + lane;
+      x[u] = q < q1 ? keys(q) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = c0 + 32 * u + lane;
-      const bool is_eq = i < w1 && (x[u] & mask) == prefix;
-      const uint32_t be = __ballot_sync(0xFFFFFFFFu, is_eq);
-      const bool take = i < w1 && ((x[u] & mask) > prefix || (is_eq && ties + __popc(be & below) < quota));
-      const uint32_t bt = __ballot_sync(0xFFFFFFFFu, take);
-      if (take) out[place + __popc(bt & below)] = row0 + i;
-      place += __popc(bt);
-      ties += __popc(be);
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t k[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      bool take[4];
+      bool eq[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        take[i] = (k[i] & mask) > prefix;
+        eq[i] = (k[i] & mask) == prefix && k[i] != 0u;
+      }
+      if (__any_sync(0xFFFFFFFFu, eq[0] | eq[1] | eq[2] | eq[3])) {
+        // keys at the threshold, in row order: lane by lane, four a lane
+        uint32_t before = 0, total = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b = __ballot_sync(0xFFFFFFFFu, eq[i]);
+          before += __popc(b & below);
+          total += __popc(b);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!eq[i]) continue;
+          take[i] = ties + before < quota;
+          ++before;
+        }
+        ties += total;
+      }
+      uint32_t p = place, total = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __ballot_sync(0xFFFFFFFFu, take[i]);
+        p += __popc(b & below);
+        total += __popc(b);
+      }
+      const int32_t t = (int32_t)(t0 + 4 * (int64_t)(c0 + 32 * u + lane));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (take[i]) out[p++] = t + i;
+      place += total;
     }
   }
 }
@@ -255,8 +357,8 @@ cudaError_t launch_cache_keep(const Shape& s, const float* weight, const int32_t
   // of the 148 SMs.
   int nc = 1;
   while (nc < kMaxCluster && (int64_t)s.batch * nc * 2 <= 148 && s.n_kv >= (int64_t)nc * 2 * 4096) nc *= 2;
-  const int64_t part = (s.n_kv + nc - 1) / nc;
-  const size_t smem = sizeof(Shared) + 4 * (size_t)(part < kStaged ? part : kStaged);
+  const int64_t part = (s.n_kv + 3 + nc - 1) / nc + 4;  // keys of a part at the most: whole groups of four
+  const size_t smem = sizeof(Shared) + 4 * (size_t)(part < kStaged ? (part + 3) / 4 * 4 : kStaged);
   cudaError_t e = ensure_smem((const void*)cache_keep_kernel, (int)(sizeof(Shared) + 4 * (size_t)kStaged));
   if (e != cudaSuccess) return e;
   if (nc > 8) {
