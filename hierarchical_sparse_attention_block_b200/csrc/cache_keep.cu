@@ -48,6 +48,13 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0xFFFFFFFFu : k;
 }
 
+// Adds 1 to a shared counter where `hit` holds, without a branch.
+__device__ __forceinline__ void count_if(bool hit, uint32_t counter) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n @p red.shared.add.u32 [%1], 1;\n}\n" ::"r"((uint32_t)hit),
+               "r"(counter)
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     cache_keep_kernel(const float* __restrict__ weight, const int32_t* kv_len, int64_t n_kv, int budget, int n_first,
                       int n_recent, int32_t* __restrict__ keep_idx, int32_t* kept_len, int32_t* __restrict__ status) {
@@ -112,9 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool few = false;  // the keys that match 16 bits of the threshold are collected
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    auto count = [&](uint32_t k) {
-      if ((k & mask) == prefix) atomicAdd(&sm.copies[(k >> shift) & 255u][lane], 1u);
-    };
+    const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(&sm.copies[0][lane]);
+    auto count = [&](uint32_t k) { count_if((k & mask) == prefix, mine_at + ((k >> shift) & 255u) * 128u); };
     if (pass == 0) {
       for (int c0 = 0; c0 < n; c0 += 4 * kThreads) {
         uint4 x[4];
@@ -128,29 +134,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int q = c0 + u * kThreads + tid;
           if (q >= n) continue;
           if (q < staged) held[q] = x[u];
-          atomicAdd(&sm.copies[x[u].x >> 24][lane], 1u);
-          atomicAdd(&sm.copies[x[u].y >> 24][lane], 1u);
-          atomicAdd(&sm.copies[x[u].z >> 24][lane], 1u);
-          atomicAdd(&sm.copies[x[u].w >> 24][lane], 1u);
-        }
-      }
-    } else if (few) {
-      for (int i = tid; i < (int)sm.n_few; i += kThreads) count(sm.few_key[i]);
-    } else {
-      for (int c0 = 0; c0 < n; c0 += 4 * kThreads) {
-        uint4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int q = c0 + u * kThreads + tid;
-          x[u] = q < n ? keys(q) : make_uint4(0u, 0u, 0u, 0u);  // (0 may match only where no key is taken)
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
           count(x[u].x);
           count(x[u].y);
           count(x[u].z);
           count(x[u].w);
         }
+      }
+    } else if (few) {
+      for (int i = tid; i < (int)sm.n_few; i += kThreads) count(sm.few_key[i]);
+    } else {
+      auto four = [&](uint4 x) {
+        count(x.x);
+        count(x.y);
+        count(x.z);
+        count(x.w);
+      };
+#pragma unroll 4
+      for (int q = tid; q < staged; q += kThreads) four(held[q]);
+      for (int c0 = staged; c0 < n; c0 += 4 * kThreads) {
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = c0 + u * kThreads + tid;
+          x[u] = q < n ? fetch(q) : make_uint4(0u, 0u, 0u, 0u);  // (0 may match only where no key is taken)
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) four(x[u]);
       }
     }
     __syncthreads();
@@ -221,13 +230,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t k[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          bool hit = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             gt += (k[i] & mask) > prefix;
-            if ((k[i] & mask) == prefix && k[i] != 0u) {
-              const uint32_t p = atomicAdd(&sm.n_few, 1u);
-              sm.few_key[p] = k[i];
-              sm.few_warp[p] = (uint16_t)warp;
+            hit |= (k[i] & mask) == prefix;
+          }
+          if (hit) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((k[i] & mask) == prefix && k[i] != 0u) {
+                const uint32_t p = atomicAdd(&sm.n_few, 1u);
+                sm.few_key[p] = k[i];
+                sm.few_warp[p] = (uint16_t)warp;
+              }
             }
           }
         }
