@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       agree();  // the rows' state
       if (!ok) break;
       ++seg;
+      float* scores = args.scores && row0 < R ? args.scores + ((seq * Hkv + g) * R + row0) * args.score_stride + r : nullptr;
       float l[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) l[i] = 0.f;
@@ -321,11 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool up = false;
           uint32_t s[NR];
           load(s);
-          if (args.scores) {
+          if (scores) {
 #pragma unroll
             for (int i = 0; i < NR; ++i)
-              if (row0 + i < R)
-                args.scores[((seq * Hkv + g) * R + row0 + i) * args.score_stride + t0 + r] = __uint_as_float(s[i]) * qscale;
+              if (row0 + i < R) scores[i * args.score_stride + t0] = __uint_as_float(s[i]) * qscale;
           }
 #pragma unroll
           for (int i = 0; i < NR; i += 2) {
