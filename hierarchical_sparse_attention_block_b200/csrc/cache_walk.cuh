@@ -1,7 +1,9 @@
 // How the kernels over a cache share their work: every key tile of every item (a part of one
 // sequence's work that reads all its key tiles) is a unit, the units lie in the order sequence, item,
 // key tile, and CTA c takes the c-th of equal contiguous ranges.  The ranges follow from the lengths
-// on the device, so ragged caches balance and one long cache covers every SM.
+// on the device, so ragged caches balance and one long cache covers every SM.  An item starts with a few
+// units more that hold no tile: what it costs a CTA to go over to another item (its query rows, the
+// products' start and end), so that a CTA with the ends of two items gets fewer tiles.
 #pragma once
 
 #include "common.cuh"
@@ -29,14 +31,16 @@ __device__ __forceinline__ int64_t range_of(int64_t u, int64_t units, int64_t ct
 struct Walk {
   const int32_t* kv_len;
   int64_t n_kv, u, u1, first;  // first: the range's begin
-  int64_t P;                   // key tiles of the sequences before s
+  int64_t P;                   // units per item of the sequences before s, summed
   int64_t L, tiles;
   int64_t L_next;              // of sequence s + 1: its load is long over when the walk gets there
   int s, T, per_seq, batch;    // per_seq: items of a sequence
+  int lead;                    // units without a tile in front of an item
   // the segment: key tiles [j0, j0 + n) of the item
   int item, j0, n;
   int64_t start;
 
+  __device__ int64_t length() const { return tiles > 0 ? tiles + lead : 0; }  // units of an item
   __device__ void at(int seq, int64_t len) {
     s = seq;
     L = len;
@@ -44,17 +48,20 @@ struct Walk {
     if (seq + 1 < batch) L_next = context_len(kv_len, seq + 1, T, n_kv);
   }
   __device__ bool next() {
-    if (u >= u1) return false;
-    while (u >= (P + tiles) * per_seq) {
-      P += tiles;
-      at(s + 1, L_next);
-    }
-    const int64_t rel = u - P * per_seq;
-    item = (int)(rel / tiles);
-    j0 = (int)(rel - (int64_t)item * tiles);
-    n = (int)min(tiles - j0, u1 - u);
-    start = u;
-    u += n;
+    do {
+      if (u >= u1) return false;
+      while (u >= (P + length()) * per_seq) {
+        P += length();
+        at(s + 1, L_next);
+      }
+      const int64_t rel = u - P * per_seq;
+      item = (int)(rel / length());
+      const int64_t from = rel - item * length(), to = min(length(), from + (u1 - u));
+      j0 = (int)max((int64_t)0, from - lead);
+      n = (int)max((int64_t)0, to - lead) - j0;
+      start = u;
+      u += to - from;
+    } while (n == 0);
     return true;
   }
   __device__ bool whole() const { return j0 == 0 && n == tiles; }
@@ -67,11 +74,20 @@ struct WalkShared {
   int64_t sums[NT / 32], found[2];
 };
 
-// The CTA's walk; all NT threads call, two barriers.  prefix (nullable, [batch + 1]): CTA 0 writes the
-// key tiles of the sequences before each, and of all; it also flags lengths out of range.
+// Key tiles (low 44 bits) and sequences that have any (high 20 bits), as one number to be summed.
+__device__ __forceinline__ int64_t tile_sum(int64_t L, int T) {
+  const int64_t n = key_tiles(L, T);
+  return n | (n > 0 ? (int64_t)1 << 44 : 0);
+}
+__device__ __forceinline__ int64_t tiles_of(int64_t sum) { return sum & (((int64_t)1 << 44) - 1); }
+__device__ __forceinline__ int64_t units_of(int64_t sum, int lead) { return tiles_of(sum) + lead * (sum >> 44); }
+
+// The CTA's walk; all NT threads call, two barriers.  lead: units without a tile in front of an item,
+// where a CTA has at least 8 tiles (else none).  prefix (nullable, [batch + 2]): CTA 0 writes the units per
+// item of the sequences before each, of all, and the lead; it also flags lengths out of range.
 template <int NT>
-__device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch, int per_seq, WalkShared<NT>& sm,
-                           int64_t* prefix, int32_t* status) {
+__device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch, int per_seq, int lead,
+                           WalkShared<NT>& sm, int64_t* prefix, int32_t* status) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // every thread counts the key tiles of a run of sequences
   const int run = (batch + NT - 1) / NT;
@@ -81,7 +97,7 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
   for (int s = s0; s < s1; ++s) {
     const int64_t L = context_len(kv_len, s, T, n_kv);
     bad = bad || L < 0;
-    mine += key_tiles(L, T);
+    mine += tile_sum(L, T);
   }
   if (bad && status && blockIdx.x == 0) atomicOr(status, kStatusBadIndex);
   int64_t incl = mine;
@@ -92,13 +108,15 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
   }
   if (lane == 31) sm.sums[warp] = incl;
   __syncthreads();
-  int64_t before = incl - mine, total = 0;
+  int64_t before_sum = incl - mine, total_sum = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     const int64_t x = sm.sums[w];
-    if (w < warp) before += x;
-    total += x;
+    if (w < warp) before_sum += x;
+    total_sum += x;
   }
+  if (tiles_of(total_sum) * per_seq < 8 * (int64_t)gridDim.x) lead = 0;
+  const int64_t before = units_of(before_sum, lead), total = units_of(total_sum, lead);
   const int64_t units = total * per_seq, ctas = range_ctas(units, gridDim.x);
   const bool busy = blockIdx.x < ctas;
   Walk walk;
@@ -107,12 +125,13 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
   walk.T = T;
   walk.per_seq = per_seq;
   walk.batch = batch;
+  walk.lead = lead;
   walk.u = walk.first = busy ? range_begin(blockIdx.x, units, ctas) : 0;
   walk.u1 = busy ? range_begin(blockIdx.x + 1, units, ctas) : 0;
-  if (busy && walk.u >= before * per_seq && walk.u < (before + mine) * per_seq) {
+  if (busy && walk.u >= before * per_seq && walk.u < (before + units_of(mine, lead)) * per_seq) {
     int64_t P = before;
     for (int s = s0; s < s1; ++s) {
-      const int64_t n = key_tiles(context_len(kv_len, s, T, n_kv), T);
+      const int64_t n = units_of(tile_sum(context_len(kv_len, s, T, n_kv), T), lead);
       if (walk.u < (P + n) * per_seq) {
         sm.found[0] = s;
         sm.found[1] = P;
@@ -125,9 +144,12 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
     int64_t P = before;
     for (int s = s0; s < s1; ++s) {
       prefix[s] = P;
-      P += key_tiles(context_len(kv_len, s, T, n_kv), T);
+      P += units_of(tile_sum(context_len(kv_len, s, T, n_kv), T), lead);
     }
-    if (tid == 0) prefix[batch] = total;
+    if (tid == 0) {
+      prefix[batch] = total;
+      prefix[batch + 1] = lead;
+    }
   }
   __syncthreads();
   if (busy) {

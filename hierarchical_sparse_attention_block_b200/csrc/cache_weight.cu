@@ -38,6 +38,7 @@ using namespace tc;
 constexpr int kKeys = kTileKeys;
 constexpr int kQRows = 128;         // query rows of one buffer
 constexpr int kHalf = kKeys * 128;  // 64 columns of 128 rows of 16-bit values: one 128-byte swizzle span
+constexpr int kLead = 2;  // what another item costs a CTA, in key tiles
 constexpr int kReadout = 256, kLoaders = 128;
 constexpr int kThreads = kReadout + kLoaders + 64;
 constexpr int kWarpQ = 8, kWarpK = 12, kWarpMMA = 13;
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   tc_fence_before();
-  Walk walk = walk_begin<kThreads>(kv_len, n_kv, T, batch, groups,
+  Walk walk = walk_begin<kThreads>(kv_len, n_kv, T, batch, groups, kLead,
                                    *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), nullptr, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

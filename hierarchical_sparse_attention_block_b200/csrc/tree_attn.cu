@@ -46,6 +46,9 @@ using namespace tc;
 
 constexpr uint32_t kTmemCols = 512;
 
+// What another item costs a CTA, in key tiles (a tile takes about 1.5 us with one row tile, 2.5 with two).
+template <int NT>
+constexpr int kLead = NT == 1 ? 5 : 6;
 constexpr int kSoftmax = 256;  // two groups
 constexpr int kThreads = kSoftmax + 96;
 constexpr int kWarpK = 8, kWarpMMA = 9, kWarpV = 10;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   const int G = H / Hkv, R = T * G, np = (R + NT * kRows - 1) / (NT * kRows);  // items: (KV head, row-tile pair)
   tc_fence_before();
-  Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv * np,
+  Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv * np, kLead<NT>,
                                       *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(32 * (D / 16) * kSplits)
   const int G = H / Hkv, R = T * G, np = (R + tile_rows - 1) / tile_rows, blocks = (R + row_lanes - 1) / row_lanes;
   const int g = blockIdx.x / blocks, r = (blockIdx.x - g * blocks) * row_lanes + lane % row_lanes;  // query row
   const int pair = (blockIdx.x - g * blocks) * row_lanes / tile_rows;  // row_lanes divides tile_rows
-  const int64_t P = work.prefix[seq], tiles = work.prefix[seq + 1] - P, total = work.prefix[batch];
+  const int64_t P = work.prefix[seq], length = work.prefix[seq + 1] - P, total = work.prefix[batch];
   const int i = r / G;
   const int64_t row = (seq * T + i) * H + g * G + (r - i * G);
   const bool mine = r < R && lane < row_lanes && split == 0;  // writes the row
@@ -602,13 +605,14 @@ __global__ void __launch_bounds__(32 * (D / 16) * kSplits)
   st.empty = false;
 #pragma unroll
   for (int x = 0; x < 16; ++x) st.o[x] = 0.f;
-  if (tiles > 0) {
+  if (length > 0) {
     const int64_t units = total * Hkv * np, ctas = range_ctas(units, grid);
-    const int64_t u0 = P * Hkv * np + ((int64_t)g * np + pair) * tiles;
-    const int64_t first = range_of(u0, units, ctas), last = range_of(u0 + tiles - 1, units, ctas);
+    const int64_t u0 = P * Hkv * np + ((int64_t)g * np + pair) * length;
+    // the CTAs that hold the item's first and last tile
+    const int64_t first = range_of(u0 + work.prefix[batch + 1], units, ctas), last = range_of(u0 + length - 1, units, ctas);
     if (first == last) return;  // written by that CTA
     const int n = (int)(last - first) + 1;
-    const int first_slot = range_begin(first, units, ctas) == u0 ? 0 : 1;
+    const int first_slot = range_begin(first, units, ctas) >= u0 ? 0 : 1;
     const int groups = 32 / row_lanes * kSplits, pr = min(r, R - 1) - pair * tile_rows;
 #pragma unroll 2
     for (int p = split * (32 / row_lanes) + lane / row_lanes; p < n; p += groups) {
@@ -722,7 +726,7 @@ Layout layout(const Shape& s, bool with_weight) {
   const size_t rows = (size_t)kMaxCtas * 2 * row_tiles(s) * kRows;
   Layout L;
   L.prefix = 0;
-  L.part_o = up((size_t)(s.batch + 1) * sizeof(int64_t));
+  L.part_o = up((size_t)(s.batch + 2) * sizeof(int64_t));
   L.part_ml = L.part_o + up(rows * s.d * sizeof(float));
   L.lse = L.part_ml + up(rows * sizeof(float2));
   L.weight = L.lse + (with_weight ? up((size_t)s.n_query * s.H * sizeof(float)) : 0);

@@ -17,7 +17,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // What the CTAs share with the merge: the unit ranges and the partial results.
 struct Work {
-  int64_t* prefix;  // [b + 1] key tiles of the sequences before; the total at the end
+  int64_t* prefix;  // [b + 2] units per item of the sequences before, of all, units in front of an item's tiles
   float4* part_o;   // [cta][2][D / 4][rows of an item]: four columns of a row; neighbours are rows
   float2* part_ml;  // [cta][2][rows of an item]: max (log2 domain), sum; (+inf, 0): the row's slot is empty
 };

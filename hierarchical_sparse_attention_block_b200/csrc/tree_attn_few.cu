@@ -29,6 +29,7 @@ namespace {
 
 using namespace tc;
 
+constexpr int kLead = 4;       // what another item costs a CTA, in key tiles of about 1.5 us
 constexpr int kSoftmax = 256;  // two groups
 constexpr int kThreads = kSoftmax + 96;
 constexpr int kWarpK = 8, kWarpMMA = 9, kWarpV = 10;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < N) slots[tid] = (int16_t)(min(tid, R - 1) / G);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   tc_fence_before();
-  Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv,
+  Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv, kLead,
                                    *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), args.work.prefix, status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
