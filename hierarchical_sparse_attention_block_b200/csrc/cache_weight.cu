@@ -384,13 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t qt = sb + (uint32_t)(qb * C::kTile + hd * ch.pitch * 128);
                 if (elect_one()) {
 #pragma unroll
-                for (int h2 = 0; h2 < D / 64; ++h2)
+                  for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + 128u * (uint32_t)buf, desc_kmajor_sw128(kt + h2 * kHalf + kk * 32),
-                              desc_kmajor_sw128(qt + h2 * kHalf + kk * 32), idesc, (h2 | kk) ? 1u : 0u);
-                umma_commit(bar(C::B_SFULL + buf));
-                umma_commit(bar(C::B_KEMPTY + s));
+                    for (int kk = 0; kk < 4; ++kk)
+                      umma_bf16(tmem + 128u * (uint32_t)buf, desc_kmajor_sw128(kt + h2 * kHalf + kk * 32),
+                                desc_kmajor_sw128(qt + h2 * kHalf + kk * 32), idesc, (h2 | kk) ? 1u : 0u);
+                  umma_commit(bar(C::B_SFULL + buf));
+                  umma_commit(bar(C::B_KEMPTY + s));
                 }
                 ++made[e];
                 ++kit;
@@ -418,12 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int L = (int)walk.L;
       Chunks ch = chunks_of(walk.item, n_counted[sp] * G);
       float* out = groups == 1 ? weight + seq * n_kv : part + ((int64_t)walk.item * batch + seq) * n_kv;
-      // One fill's sum of a key joins what the fills before left.
-      auto add = [&](int c, int t, float sum) {
-        if (t >= L + T) return;
-        if (c > 0 || (groups == 1 && t < L)) sum += out[t];
-        out[t] = sum;
-      };
       for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
         ch.at(c);
         const int qb = fill & 1;
@@ -432,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = (walk.j0 + x) * kKeys + r;
           const bool tail = (walk.j0 + x + 1) * kKeys > L;
           const int j = t - L;  // drafted row, from the context's end on
-          float sum = 0.f;
+          const int j_word = min(max(j, 0) >> 5, kDraftWords - 1), j_bit = j & 31;
+          // One fill's sum of a key joins what the fills before left; read while the products are formed.
+          float sum = t < L + T && (c > 0 || (groups == 1 && t < L)) ? out[t] : 0.f;
           for (int hd = 0; ok && hd < ch.n; ++hd, ++got) {
             const int buf = got & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + 2 * e + buf), (uint32_t)(got >> 1) & 1u, abort_flag));
@@ -462,15 +458,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                   continue;
                 }
+                // Padding, rows that add nothing, and, for a drafted row, the slots not below it in the tree.
+                // No branch a column: a CTA with a tile behind the context is the one all others wait for
+                // (1 x 8K keys, 1024 rows a KV head: 170 us with a test for each column, 93 this way).
+                uint32_t hidden = none;
+                if (tail) {
+                  uint32_t seen = 0;
+                  if (parent) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      seen |= (tree.anc[rows.slot[at + i]][j_word] >> j_bit & 1u) << i;
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) seen |= (j <= rows.slot[at + i] ? 1u : 0u) << i;
+                  }
+                  hidden |= j < 0 ? 0u : ~seen;
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  bool see = !((none >> i) & 1u);
-                  if (tail && j >= 0) {  // a drafted row: only the slots below it in the tree see it
-                    const int slot = rows.slot[at + i];
-                    see = see && (parent ? j < T && ((tree.anc[slot][j >> 5] >> (j & 31)) & 1u) : j <= slot);
-                  }
                   const float p = fast_exp2(fmaf(__uint_as_float(s[16 * h + i]), qscale, nl[i]));
-                  acc[i & 1].x += see ? p : 0.f;
+                  acc[i & 1].x += (hidden >> i) & 1u ? 0.f : p;
                 }
               }
             };
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc[0] = fadd2(acc[0], acc[1]);
             sum += acc[0].x + acc[0].y;
           }
-          if (ok) add(c, t, sum);
+          if (ok && t < L + T) out[t] = sum;
         }
         mbar_arrive(bar(C::B_QEMPTY + qb));
       }
