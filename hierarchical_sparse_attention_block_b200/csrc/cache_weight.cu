@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg = 0, fill = 0;
     auto sync = [&]() {
       mbar_arrive(bar(C::B_LSYNC));
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_LSYNC), lphase, abort_flag)) && ok;
+      ok = warp_wait_or_abort(bar(C::B_LSYNC), lphase, abort_flag) && ok;
       lphase ^= 1u;
     };
     while (ok && walk.next()) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       DraftTree& tree = trees[sp];
       int16_t* list = lists + sp * kMaxDraft;
       if (seg >= 2) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFREE + sp), (uint32_t)((seg >> 1) - 1) & 1u, abort_flag));
+        ok = warp_wait_or_abort(bar(C::B_SEGFREE + sp), (uint32_t)((seg >> 1) - 1) & 1u, abort_flag);
         if (!ok) break;
       }
       bool bad = false;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ch.at(c);
         const int b = fill & 1;
         if (fill >= 2) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_QEMPTY + b), (uint32_t)((fill >> 1) - 1) & 1u, abort_flag));
+          ok = warp_wait_or_abort(bar(C::B_QEMPTY + b), (uint32_t)((fill >> 1) - 1) & 1u, abort_flag);
           if (!ok) break;
         }
         constexpr int CH = D / 8;  // 16-byte chunks of a row
@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
     {
-      auto waited = [&](uint32_t barrier, uint32_t parity) {  // the warp stays together
-        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(barrier, parity, abort_flag)) != 0;
+      auto waited = [&](uint32_t barrier, uint32_t parity) {
+        return warp_wait_or_abort(barrier, parity, abort_flag);
       };
       bool ok = true;
       int seg = 0, fill = 0, kit = 0;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int seg = 0, fill = 0, got = 0;
     while (ok && walk.next()) {
       const int sp = seg & 1;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SEGFULL + sp), (uint32_t)(seg >> 1) & 1u, abort_flag));
+      ok = warp_wait_or_abort(bar(C::B_SEGFULL + sp), (uint32_t)(seg >> 1) & 1u, abort_flag);
       ++seg;
       if (!ok) break;
       const DraftTree& tree = trees[sp];
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; ok && c < ch.chunks; ++c, ++fill) {
         ch.at(c);
         const int qb = fill & 1;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_QFULL + qb), (uint32_t)(fill >> 1) & 1u, abort_flag));
+        ok = warp_wait_or_abort(bar(C::B_QFULL + qb), (uint32_t)(fill >> 1) & 1u, abort_flag);
         for (int x = e; ok && x < walk.n; x += 2) {
           const int t = (walk.j0 + x) * kKeys + r;
           const bool tail = (walk.j0 + x + 1) * kKeys > L;
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sum = t < L + T && (c > 0 || (groups == 1 && t < L)) ? out[t] : 0.f;
           for (int hd = 0; ok && hd < ch.n; ++hd, ++got) {
             const int buf = got & 1;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + 2 * e + buf), (uint32_t)(got >> 1) & 1u, abort_flag));
+            ok = warp_wait_or_abort(bar(C::B_SFULL + 2 * e + buf), (uint32_t)(got >> 1) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const Rows& rows = rows_of[qb];
@@ -452,8 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (none == 0 && !tail) {
 #pragma unroll
                   for (int i = 0; i < 8; ++i) {
-                    const float2 x = ffma2(make_float2(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])),
-                                           qs2, make_float2(nl[2 * i], nl[2 * i + 1]));
+                    const uint32_t* z = s + 16 * h + 2 * i;
+                    const float2 x = ffma2(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), qs2,
+                                           make_float2(nl[2 * i], nl[2 * i + 1]));
                     acc[i & 1] = fadd2(acc[i & 1], make_float2(fast_exp2(x.x), fast_exp2(x.y)));
                   }
                   continue;

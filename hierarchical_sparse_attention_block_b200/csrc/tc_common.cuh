@@ -74,6 +74,11 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
   }
 }
 
+// mbar_wait_or_abort of a whole warp, which stays together: the answer is the same for all lanes.
+__device__ __forceinline__ bool warp_wait_or_abort(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar, parity, abort)) != 0;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -300,14 +305,6 @@ __device__ __forceinline__ void tmem_st16_issue(uint32_t addr, const uint32_t (&
       "%15, %16};" ::"r"(addr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-// Zeros into 32 consecutive TMEM columns of this warp's 32 lanes; complete it with tmem_wait_st.
-__device__ __forceinline__ void tmem_zero32_issue(uint32_t addr) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, "
-      "%1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(addr),
-      "r"(0)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

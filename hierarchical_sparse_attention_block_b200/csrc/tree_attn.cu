@@ -5,19 +5,16 @@
 //
 // The T tokens of a sequence and the G = H / Hk heads of one KV head make R = T G query rows that
 // read the same K and V.  With few rows the call is bound by the cache's bytes, with many (R above
-// about 128) by the tensor cores; one kernel serves both: tiles of 128 query rows (padded) against
-// tiles of 128 keys.  A tile of 128 x 128 costs the tensor cores about half the time that its K and V
-// take from HBM, so the padding of few rows costs nothing; R above 128 puts two row tiles on one CTA,
-// which then reads every K/V tile once for 256 rows.
+// about 128) by the tensor cores.  Up to 16 rows are tree_attn_few.cu's; here tiles of 128 query rows
+// (padded) meet tiles of 128 keys.  A tile of 128 x 128 costs the tensor cores about half the time that
+// its K and V take from HBM, so the padding of 17 to 128 rows costs little; R above 128 puts two row
+// tiles on one CTA, which then reads every K/V tile once for 256 rows.
 //
 // Work.  A unit is one key tile of one (sequence, KV head, row-tile pair) item.  All units of the
 // call, in that order, are cut into equal contiguous ranges, one per CTA (one CTA per SM), from the
 // lengths on the device: ragged caches balance, and a long cache of a single sequence covers every
 // SM.  An item that one CTA holds whole is written by it; the others leave (max, sum, unnormalised
 // output) per range in the workspace, merged by tree_attn_merge_kernel.
-//
-// This file's kernel takes 17 query rows and more of a KV head, one or two tiles of 128 rows at a time;
-// tree_attn_few.cu up to 16, with the keys as the product's rows.
 //
 // Roles of a CTA: two softmax groups of four warps, one thread per query row (TMEM lane = row); then
 // one thread each for the K loads (TMA), the MMAs (tcgen05) and the V loads.  Two row tiles: each
@@ -104,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  uint32_t* odd_rows = misc + 2;  // [2][kDraftWords]: drafted V rows with values that are not finite, per segment parity
+  uint32_t* odd_rows = misc + 2;  // [2][kDraftWords] by segment parity: drafted V rows not all finite
   auto fail = [&]() {
     *abort_flag = 1;
     if (status) atomicOr(status, kStatusTimeout);
@@ -129,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = H / Hkv, R = T * G, np = (R + NT * kRows - 1) / (NT * kRows);  // items: (KV head, row-tile pair)
   tc_fence_before();
   Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv * np, kLead<NT>,
-                                      *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), work.prefix, status);
+                                   *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), work.prefix,
+                                   status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -174,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
     {
-      auto waited = [&](uint32_t barrier, uint32_t parity) {  // the warp stays together
-        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(barrier, parity, abort_flag)) != 0;
+      auto waited = [&](uint32_t barrier, uint32_t parity) {
+        return warp_wait_or_abort(barrier, parity, abort_flag);
       };
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q and K both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // weights (tensor memory), V MN-major
@@ -192,12 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t qb = sb + (uint32_t)(NT == 2 ? t * C::kTile : 0);
         if (elect_one()) {
 #pragma unroll
-        for (int h2 = 0; h2 < D / 64; ++h2)
+          for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + 128u * (uint32_t)t, desc_kmajor_sw128(qb + h2 * kHalf + kk * 32),
-                      desc_kmajor_sw128(kt + h2 * kHalf + kk * 32), kIdS, (h2 | kk) ? 1u : 0u);
-        umma_commit(bar(C::B_SFULL + t));
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(tmem + 128u * (uint32_t)t, desc_kmajor_sw128(qb + h2 * kHalf + kk * 32),
+                        desc_kmajor_sw128(kt + h2 * kHalf + kk * 32), kIdS, (h2 | kk) ? 1u : 0u);
+          umma_commit(bar(C::B_SFULL + t));
         }
       };
       auto free_k = [&]() {
@@ -208,10 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t vt = sb + (uint32_t)(C::V_OFF + (vit % C::VS) * C::kTile);
         if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
-          umma_bf16_ta(tmem + col_o(t), tmem + 128u * (uint32_t)t + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1)),
-                       desc_mnmajor_sw128(vt + kk * 2048, kHalf), kIdO, (!first || kk) ? 1u : 0u);
-        umma_commit(bar(C::B_PFREE + t));
+          for (int kk = 0; kk < kRows / 16; ++kk)
+            umma_bf16_ta(tmem + col_o(t), tmem + 128u * (uint32_t)t + (uint32_t)(32 * (kk >> 1) + 8 * (kk & 1)),
+                         desc_mnmajor_sw128(vt + kk * 2048, kHalf), kIdO, (!first || kk) ? 1u : 0u);
+          umma_commit(bar(C::B_PFREE + t));
         }
         ++cnt[t];
       };
@@ -303,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sync_phase = 0;
     auto sync = [&]() {
       mbar_arrive(bar(C::B_SYNC));
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SYNC), sync_phase, abort_flag)) && ok;
+      ok = warp_wait_or_abort(bar(C::B_SYNC), sync_phase, abort_flag) && ok;
       sync_phase ^= 1u;
     };
     while (ok && walk.next()) {
@@ -354,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = (walk.j0 + x) * kRows;
         const bool tail = t0 + kRows > L;
         if (t == 0 && x == ahead_at) prefetch_next<D>(walk, args, np, NT * kRows, r);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + t), (uint32_t)cnt & 1u, abort_flag));
+        ok = warp_wait_or_abort(bar(C::B_SFULL + t), (uint32_t)cnt & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (warp_rows) {
@@ -429,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           weigh(1, xb);
           l2 = fadd2(l2, fadd2(ls[0], ls[1]));
           if (__any_sync(0xFFFFFFFFu, resc)) {  // the group's output holds earlier tiles: rescale it once they are in
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag))) {
+            if (!warp_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag)) {
               ok = false;
               break;
             }
@@ -449,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V rows behind the context.  The scores are in, and with them this
           // group's product before, so the wait cannot take an earlier fill of the V slot for this one.
           const int vs = (vit0 + x) % C::VS;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)((vit0 + x) / C::VS) & 1u, abort_flag));
+          ok = warp_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)((vit0 + x) / C::VS) & 1u, abort_flag);
           if (!ok) break;
           clear_tail_values<D>(smem + C::V_OFF + vs * C::kTile, t0, L, T, parent != nullptr, tree, odd, r);
           fence_async_smem();
@@ -461,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (any) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag));
+        ok = warp_wait_or_abort(bar(C::B_PFREE + t), (uint32_t)(cnt - 1) & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
       }
@@ -609,7 +607,8 @@ __global__ void __launch_bounds__(32 * (D / 16) * kSplits)
     const int64_t units = total * Hkv * np, ctas = range_ctas(units, grid);
     const int64_t u0 = P * Hkv * np + ((int64_t)g * np + pair) * length;
     // the CTAs that hold the item's first and last tile
-    const int64_t first = range_of(u0 + work.prefix[batch + 1], units, ctas), last = range_of(u0 + length - 1, units, ctas);
+    const int64_t first = range_of(u0 + work.prefix[batch + 1], units, ctas);
+    const int64_t last = range_of(u0 + length - 1, units, ctas);
     if (first == last) return;  // written by that CTA
     const int n = (int)(last - first) + 1;
     const int first_slot = range_begin(first, units, ctas) >= u0 ? 0 : 1;

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* raise_flag = reinterpret_cast<volatile int*>(misc + 2);  // [2]: a row of the group exceeds its max
-  uint32_t* odd_rows = misc + 4;  // [2][kDraftWords]: drafted V rows with values that are not finite, per segment parity
+  uint32_t* odd_rows = misc + 4;  // [2][kDraftWords] by segment parity: drafted V rows not all finite
   auto fail = [&]() {
     *abort_flag = 1;
     if (status) atomicOr(status, kStatusTimeout);
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote, and read of the workspace
   tc_fence_before();
   Walk walk = walk_begin<kThreads>(args.kv_len, n_kv, T, args.batch, Hkv, kLead,
-                                   *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), args.work.prefix, status);
+                                   *reinterpret_cast<WalkShared<kThreads>*>(smem + C::WALK_OFF), args.work.prefix,
+                                   status);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -154,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_expect_tx(bar(full + slot), C::kTile);
 #pragma unroll
           for (int h2 = 0; h2 < D / 64; ++h2)
-            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, walk.item, (walk.j0 + x) * kRows, walk.s, bar(full + slot), policy);
+            tma_load_4d(dst + h2 * kHalf, map, 64 * h2, walk.item, (walk.j0 + x) * kRows, walk.s, bar(full + slot),
+                        policy);
           ++issued;
           if (++slot == NS) {
             slot = 0;
@@ -168,13 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMMA) {
     // ---------------- MMA issuer ----------------
     {
-      auto waited = [&](uint32_t barrier, uint32_t parity) {  // the warp stays together
-        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(barrier, parity, abort_flag)) != 0;
+      auto waited = [&](uint32_t barrier, uint32_t parity) {
+        return warp_wait_or_abort(barrier, parity, abort_flag);
       };
       constexpr uint32_t kIdS = idesc_bf16(kRows, N, false, false);  // K and Q both K-major
       constexpr uint32_t kIdO = idesc_bf16(128, N, true, false);     // V with its columns as rows, weights K-major
       bool ok = true;
-      int kit = 0, vit = 0, seg = 0;  // K and V tiles taken so far (the score and weight buffers go with them), segments
+      int kit = 0, vit = 0, seg = 0;  // K and V tiles taken (the score and weight buffers go with them), segments
       auto scores_of = [&]() {        // of the K tile kit
         const uint32_t kt = sb + (uint32_t)(C::K_OFF + (kit % C::KS) * C::kTile);
         if (elect_one()) {
@@ -255,12 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sync_phase = 0, agree_phase = 0;
     auto sync = [&]() {
       mbar_arrive(bar(C::B_SYNC));
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SYNC), sync_phase, abort_flag)) && ok;
+      ok = warp_wait_or_abort(bar(C::B_SYNC), sync_phase, abort_flag) && ok;
       sync_phase ^= 1u;
     };
     auto agree = [&]() {
       mbar_arrive(bar(C::B_AGREE + t));
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_AGREE + t), agree_phase, abort_flag)) && ok;
+      ok = warp_wait_or_abort(bar(C::B_AGREE + t), agree_phase, abort_flag) && ok;
       agree_phase ^= 1u;
     };
     while (ok && walk.next()) {
@@ -294,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       agree();  // the rows' state
       if (!ok) break;
       ++seg;
-      float* scores = args.scores && row0 < R ? args.scores + ((seq * Hkv + g) * R + row0) * args.score_stride + r : nullptr;
+      float* scores =
+          args.scores && row0 < R ? args.scores + ((seq * Hkv + g) * R + row0) * args.score_stride + r : nullptr;
       float l[NR];
 #pragma unroll
       for (int i = 0; i < NR; ++i) l[i] = 0.f;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = t0 + kRows > L;
         const int j = t0 + r - L;  // drafted row of this key, from the context's end on
         if (t == 0 && x == ahead_at) prefetch_next<D>(walk, args, 1, kFewRows, r);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_SFULL + buf), (uint32_t)(cnt >> 1) & 1u, abort_flag));
+        ok = warp_wait_or_abort(bar(C::B_SFULL + buf), (uint32_t)(cnt >> 1) & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
         // the rows' scores of this key, -inf where a row does not see it
@@ -331,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < NR; i += 2) {
             const float4 st = *reinterpret_cast<const float4*>(rows + i);
-            const float x0 = fmaf(__uint_as_float(s[i]), qscale, -st.x), x1 = fmaf(__uint_as_float(s[i + 1]), qscale, -st.z);
+            const float x0 = fmaf(__uint_as_float(s[i]), qscale, -st.x);
+            const float x1 = fmaf(__uint_as_float(s[i + 1]), qscale, -st.z);
             up |= x0 > st.y;
             up |= x1 > st.w;
             p[i] = fast_exp2(x0);  // 0 where masked
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < NR; ++i) l[i] *= alphas[i];
           if (x > 0) {  // the output holds earlier tiles: rescale it once they are in
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + (buf ^ 1)), (uint32_t)((cnt - 1) >> 1) & 1u, abort_flag));
+            ok = warp_wait_or_abort(bar(C::B_PFREE + (buf ^ 1)), (uint32_t)((cnt - 1) >> 1) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
             uint32_t ov[NR];
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         // the weight buffer is free once the product of two tiles ago is in
         if (cnt >= 2) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + buf), (uint32_t)((cnt >> 1) - 1) & 1u, abort_flag));
+          ok = warp_wait_or_abort(bar(C::B_PFREE + buf), (uint32_t)((cnt >> 1) - 1) & 1u, abort_flag);
           if (!ok) break;
         }
         uint8_t* at = smem + C::P_OFF + 2 * buf * C::kWeights + p_half + row0 * 128 + p_byte;
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tail && t == 0) {
           // The product of two tiles ago is in, so the wait cannot take an earlier fill of the V slot for this one.
           const int vs = cnt % C::VS;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)(cnt / C::VS) & 1u, abort_flag));
+          ok = warp_wait_or_abort(bar(C::B_VFULL + vs), (uint32_t)(cnt / C::VS) & 1u, abort_flag);
           if (!ok) break;
           clear_tail_values<D>(smem + C::V_OFF + vs * C::kTile, t0, L, T, parent != nullptr, tree, odd, r);
         }
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(C::B_PREADY + buf));
       }
       if (!ok) break;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(C::B_PFREE + ((cnt - 1) & 1)), (uint32_t)((cnt - 1) >> 1) & 1u, abort_flag));
+      ok = warp_wait_or_abort(bar(C::B_PFREE + ((cnt - 1) & 1)), (uint32_t)((cnt - 1) >> 1) & 1u, abort_flag);
       if (!ok) break;
       tc_fence_after();
       // the rows' sums: over the lanes, then over the warps
