@@ -407,10 +407,24 @@ def _on_device(call, device, stream, fn, *args):
         raise HisaError(call, rc)
 
 
-def _scratch(call, device, workspace, nbytes):
+def _empty(device, stream, shape, dtype):
+    """A new tensor on CUDA device `device` that the work of `stream` (None: the current one) may use from here on:
+    allocated on that stream, so that neither what held the memory before nor, once it is freed, what holds it next
+    meets that work; the current stream, which reads it, holds it as well."""
+    torch = _torch()
+    dev = torch.device("cuda", device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(call, device, workspace, nbytes, stream):
     """(tensor, address) of the caller's workspace, or of a new one of nbytes() bytes."""
     if workspace is None:
-        workspace = _workspace(nbytes(), _torch().device("cuda", device))
+        workspace = _empty(device, stream, max(nbytes(), 16), _torch().uint8)
     return workspace, _dense(call, device, "workspace", workspace, _torch().uint8, (workspace.numel(),))
 
 
@@ -436,7 +450,7 @@ def hisa_tree_attn_fwd(p, q, k, v, kv_len, o, lse=None, parent=None, weight=None
           _dense(call, dev, "parent", parent, i32, (b, T)), _dense(call, dev, "o", o, bf, (b, T, H, d)),
           _dense(call, dev, "lse", lse, f32, (b, T, H)), _dense(call, dev, "weight", weight, f32, (b, n)),
           _dense(call, dev, "dev_status", dev_status, i32, (1,)))
-    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_tree_attn_workspace_size(p, weight is not None))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_tree_attn_workspace_size(p, weight is not None), stream)
     _on_device(call, dev, stream, _lib.hisa_tree_attn_fwd, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
@@ -456,7 +470,7 @@ def hisa_cache_weight(p, q, k, kv_len, lse, weight, parent=None, path=None, dev_
           _dense(call, dev, "kv_len", kv_len, i32, (b,)), _dense(call, dev, "parent", parent, i32, (b, T)),
           _dense(call, dev, "path", path, i32, (b, T)), _dense(call, dev, "lse", lse, f32, (b, T, H)),
           _dense(call, dev, "weight", weight, f32, (b, n)), _dense(call, dev, "dev_status", dev_status, i32, (1,)))
-    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_weight_workspace_size(p))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_weight_workspace_size(p), stream)
     _on_device(call, dev, stream, _lib.hisa_cache_weight, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
@@ -475,7 +489,7 @@ def hisa_cache_keep(p, weight, kv_len, budget, keep_idx, kept_len, n_first=0, n_
           _dense(call, dev, "kv_len", kv_len, i32, (b,)), budget, n_first, n_recent,
           _dense(call, dev, "keep_idx", keep_idx, i32, (b, budget)),
           _dense(call, dev, "kept_len", kept_len, i32, (b,)), _dense(call, dev, "dev_status", dev_status, i32, (1,)))
-    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_keep_workspace_size(p))
+    ws, ws_at = _scratch(call, dev, workspace, lambda: hisa_cache_keep_workspace_size(p), stream)
     _on_device(call, dev, stream, _lib.hisa_cache_keep, ctypes.byref(p), *at, ws_at, ws.numel())
 
 
@@ -532,23 +546,25 @@ def forward(p, q_idx, k_idx, q, k, v, return_indices=False, stream=None, idx_wei
 
 def tree_attn(p, q, k, v, kv_len, parent=None, weight=None, stream=None):
     """Allocate the outputs with torch and run hisa_tree_attn_fwd; returns (o, lse)."""
-    import torch
-
-    o = torch.empty((p.batch, p.n_q, p.n_heads, p.d_head), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((p.batch, p.n_q, p.n_heads), dtype=torch.float32, device=q.device)
+    torch, dev = _torch(), _device_of("tree_attn", "q", q)
+    o = _empty(dev, stream, (p.batch, p.n_q, p.n_heads, p.d_head), torch.bfloat16)
+    lse = _empty(dev, stream, (p.batch, p.n_q, p.n_heads), torch.float32)
     hisa_tree_attn_fwd(p, q, k, v, kv_len, o, lse, parent=parent, weight=weight, stream=stream)
     return o, lse
 
 
 def evict(p, weight, kv_len, budget, arrays, n_first=0, n_recent=0, stream=None):
     """Shrink every sequence of the cache to at most `budget` rows: hisa_cache_keep on `weight` [b][n_kv], then
-    hisa_cache_compact of `arrays` ([b][n_kv][...] tensors) and of `weight`.  kv_len [b] int32 is updated in place;
-    returns the rows kept, keep_idx [b][budget].  Block keys of a moved cache have to be pooled again."""
-    import torch
-
-    keep = torch.empty((p.batch, budget), dtype=torch.int32, device=weight.device)
-    hisa_cache_keep(p, weight, kv_len, budget, keep, kv_len, n_first, n_recent, stream=stream)
+    hisa_cache_compact of `arrays` ([b][n_kv][...] tensors) and of `weight`.  kv_len [b] int32 is updated in place
+    (a refused call leaves it as it was); returns the rows kept, keep_idx [b][budget].  Block keys of a moved cache
+    have to be pooled again."""
+    torch, dev = _torch(), _device_of("evict", "weight", weight)
+    keep = _empty(dev, stream, (p.batch, max(budget, 0)), torch.int32)
+    kept = _empty(dev, stream, (p.batch,), torch.int32)
+    hisa_cache_keep(p, weight, kv_len, budget, keep, kept, n_first, n_recent, stream=stream)
     hisa_cache_compact(p, keep, [*arrays, weight], stream=stream)
+    with torch.cuda.stream(stream):
+        kv_len.copy_(kept)
     return keep
 
 

@@ -855,6 +855,12 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {  // null pointers 
     if (!hisa::aligned16(p)) return false;
   return true;
 }
+
+// Whether two arrays of n_rows rows each share bytes (a quotient: the product may pass 64 bits).
+bool rows_overlap(const hisa_rows_t& a, const hisa_rows_t& b, uint64_t n_rows) {
+  const uint64_t x = (uint64_t)(uintptr_t)a.base, y = (uint64_t)(uintptr_t)b.base;
+  return x < y ? (y - x) / (uint64_t)a.row_bytes < n_rows : (x - y) / (uint64_t)b.row_bytes < n_rows;
+}
 }  // namespace
 
 hisa_status_t hisa_tree_attn_workspace_size(const hisa_params_t* params, int32_t with_weight, size_t* bytes) {
@@ -940,6 +946,8 @@ hisa_status_t hisa_cache_compact(const hisa_params_t* params, const int32_t* row
     if (!arrays[a].base || !hisa::aligned16(arrays[a].base)) return HISA_ERR_INVALID_ARG;
     if (arrays[a].row_bytes < 4 || arrays[a].row_bytes > (1 << 24) || arrays[a].row_bytes % 4 != 0)
       return HISA_ERR_INVALID_ARG;
+    for (int other = 0; other < a; ++other)  // two sweeps over the same bytes would race
+      if (rows_overlap(arrays[a], arrays[other], (uint64_t)s.batch * (uint64_t)s.n_kv)) return HISA_ERR_INVALID_ARG;
   }
   return hisa::cuda_fail(
       hisa::launch_cache_compact(s, rows, n_rows, dst_begin, arrays, n_arrays, dev_status, stream));

@@ -324,7 +324,8 @@ hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_
  * is unchanged), so these steps have no counterpart there; they share the
  * tensors of the calls above.  `params` gives batch, n_q (T, the slots for
  * drafted tokens, 1..256; HISA_ERR_UNSUPPORTED above), n_kv (the ROWS the
- * cache has per sequence), n_heads, n_kv_heads, d_head and scale.
+ * cache has per sequence), n_heads (at most 1024), n_kv_heads, d_head and
+ * scale.
  *   kv_len [b] int32, device: context rows of each sequence; rows [0, L) of
  *     sequence s are its context (L = kv_len[s]) and row L + i holds the key
  *     and value of drafted token i.  0 <= L and L + T <= n_kv; a sequence that
@@ -408,8 +409,8 @@ typedef struct hisa_rows {
  * at or above n_kv or not greater than every in-range entry before it is
  * skipped, with bit 0 of *dev_status; its destination row stays as it is, as
  * does every row that is no destination.  A negative dst_begin[s] skips the
- * sequence the same way.  arrays: host array of 1..8 entries that do not
- * overlap.  Uses batch and n_kv of params. */
+ * sequence the same way.  arrays: host array of 1..8 entries; entries that
+ * share bytes are refused.  Uses batch and n_kv of params. */
 hisa_status_t hisa_cache_compact(const hisa_params_t* params, const int32_t* rows, int32_t n_rows,
                                  const int32_t* dst_begin, const hisa_rows_t* arrays, int32_t n_arrays,
                                  int32_t* dev_status, cudaStream_t stream);

@@ -105,6 +105,20 @@ def test_cache_compact_arguments():
     assert lib.hisa_cache_compact(ctypes.byref(p), A, 16, None, None, 1, None, None) == BAD
 
 
+@pytest.mark.parametrize("batch,n_kv,other", [
+    (2, 512, (4096, 256)),                     # the same array twice
+    (2, 512, (4096 + 2 * 512 * 256 - 16, 4)),  # begins in the last row
+    (2, 512, (4096 - 16, 4)),                  # ends in the first row
+    (65535, (1 << 31) - 1, (1 << 62, 4)),      # the size in bytes passes 64 bits with rows this long
+])
+def test_arrays_that_share_bytes_are_refused(batch, n_kv, other):
+    p = _p(batch=batch, n_kv=n_kv)
+    row = 256 if batch == 2 else 1 << 24
+    for pair in (((4096, row), other), (other, (4096, row))):
+        c = (hs.HisaRows * 2)(*[hs.HisaRows(*a) for a in pair])
+        assert hs.lib().hisa_cache_compact(ctypes.byref(p), A, 16, None, c, 2, None, None) == BAD
+
+
 class _OnGpu:
     """A stand-in for a CUDA tensor: what the binding looks at before it calls the library."""
 

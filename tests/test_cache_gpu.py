@@ -504,6 +504,109 @@ def test_bad_entries_move_nothing(hs, n):
     check_compact(hs, rows, [0, 3, n, -1, 1, 2], some_arrays(6, n_kv, n + 1, ((65,), ())))
 
 
+# ------------------------------------------------------------------ streams, graphs, refused calls
+
+def cache_of(b, T, H, Hk, d, n_kv, lens, seed):
+    """A cache and its drafted tokens on the GPU, and the front ends' steps over it as one function of a stream."""
+    g = to_gpu(make_inputs(b, T, H, Hk, d, n_kv, lens, "tree", seed, garbage=False))
+    g["position"] = torch.arange(n_kv, device="cuda").repeat(b, 1)
+    return g
+
+
+def all_steps(hs, g, H, Hk, d, budget, stream=None):
+    """Attention, weights of a path, its commit, an eviction: everything that changes or comes out."""
+    b, T = g["q"].shape[:2]
+    p = hs.params(b, T, g["k"].shape[1], 128, 128, 4, 64, H, Hk, d)
+    o, lse = hs.tree_attn(p, g["q"], g["k"], g["v"], g["kv_len"], parent=g["parent"], stream=stream)
+    hs.hisa_cache_weight(p, g["q"], g["k"], g["kv_len"], lse, g["weight"], parent=g["parent"], path=g["path"],
+                         stream=stream)
+    hs.hisa_cache_compact(p, g["rows"], [g["k"], g["v"], g["position"], g["weight"]], dst_begin=g["kv_len"],
+                          stream=stream)
+    keep = hs.evict(p, g["weight"], g["kv_len"], budget, [g["k"], g["v"], g["position"]], 4, 16, stream=stream)
+    return [o, lse, keep, g["kv_len"], g["k"], g["v"], g["position"], g["weight"]]
+
+
+def with_path(g):
+    T = g["q"].shape[1]
+    path = torch.full_like(g["parent"], -1)
+    for s in range(path.shape[0]):
+        chain = ref.ancestors(g["parent"][s].cpu(), T)[T - 1]
+        path[s, :len(chain)] = torch.tensor(chain)
+    g["path"] = path
+    g["rows"] = torch.where(path >= 0, path + g["kv_len"][:, None], -1)
+    return g
+
+
+def copy_of(g):
+    return {n: t.clone() for n, t in g.items()}
+
+
+SETS = [(2, 9, 8, 2, 128, 700, [600, 33], 200), (1, 4, 4, 4, 64, 9000, [8990], 3000)]
+
+
+def test_two_streams_at_once(hs):
+    """The steps of two caches on two streams, over and over, scratch and outputs from the front ends: as alone."""
+    kept, want = [], []
+    for i, (b, T, H, Hk, d, n_kv, lens, budget) in enumerate(SETS):
+        g = with_path(cache_of(b, T, H, Hk, d, n_kv, lens, 40 + i))
+        kept.append(g)
+        want.append([t.clone() for t in all_steps(hs, copy_of(g), H, Hk, d, budget)])
+    turns = 12
+    caches = [[copy_of(g) for _ in range(turns)] for g in kept]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for turn in range(turns):
+        for i, (b, T, H, Hk, d, n_kv, lens, budget) in enumerate(SETS):
+            out = all_steps(hs, caches[i][turn], H, Hk, d, budget, streams[i])
+            torch.cuda.current_stream().wait_stream(streams[i])
+            got[i].append([t.clone() for t in out])  # on the current stream, the originals dropped at once
+            del out
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(out, want[i]))
+
+
+def test_captured_evictions(hs):
+    """Weights, commit and eviction captured once and replayed over changing lengths, weights and paths."""
+    b, T, H, Hk, d, n_kv, lens, budget = 2, 9, 8, 2, 128, 700, [600, 33], 200
+    live = with_path(cache_of(b, T, H, Hk, d, n_kv, lens, 50))
+    all_steps(hs, copy_of(live), H, Hk, d, budget)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = all_steps(hs, live, H, Hk, d, budget)
+    for turn, lens in enumerate(([650, 5], [199, 691], [0, 210])):
+        g = with_path(cache_of(b, T, H, Hk, d, n_kv, lens, 60 + turn))
+        for n, t in g.items():
+            live[n].copy_(t)
+        graph.replay()
+        want = all_steps(hs, g, H, Hk, d, budget)
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_a_refused_eviction_changes_nothing(hs):
+    b, n_kv = 2, 300
+    p = hs.params(b, 1, n_kv, 128, 128, 4, 64)
+    weight, kv_len = torch.rand(b, n_kv, device="cuda"), torch.tensor([300, 120], dtype=torch.int32, device="cuda")
+    k = torch.randn(b, n_kv, 8, device="cuda")
+    arrays = ([k[:, ::2]], [k, k], [k, weight], [k] * 8, [k.to(torch.int8)[..., :6].contiguous()])
+    before = [t.clone() for t in (k, weight, kv_len)]
+    for a in arrays:
+        with pytest.raises(hs.HisaError):
+            hs.evict(p, weight, kv_len, 100, a)
+    with pytest.raises(hs.HisaError):
+        hs.evict(p, weight, kv_len, 0, [k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(before, (k, weight, kv_len)))
+
+
+@pytest.mark.parametrize("T,H", [(15, 1), (16, 1), (17, 1), (127, 1), (128, 1), (129, 1), (64, 4), (129, 2)])
+def test_query_rows_at_the_tiles_borders(hs, T, H):
+    x = make_inputs(2, T, H, 1, 64, 420, [420 - T, 128], "tree", seed=T + H)
+    check_tree(hs, x, H, 1, 64, True)
+
+
 # ------------------------------------------------------------------ the calls together
 
 def test_a_bounded_cache_through_a_decode(hs):
