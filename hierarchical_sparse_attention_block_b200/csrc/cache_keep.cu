@@ -5,8 +5,9 @@
 // by radix, 8 bits a pass from the top, and a sweep that emits the taken rows in order.
 //
 // A cluster of up to 16 CTAs takes one sequence, a contiguous part of its rows each, so that a single
-// long cache is not left to one SM; the first 46K keys of a part stay in shared memory, each sweep
-// reads the others again (L2).  A pass counts into 32 copies of the 256 counters, copy = lane: the
+// long cache is not left to one SM, and for a few very long ones a cooperative grid shares the whole GPU
+// among them (their counters then meet in the workspace); the first 46K keys of a part stay in shared
+// memory, each sweep reads the others again (L2).  A pass counts into 32 copies of the 256 counters, copy = lane: the
 // atomics of a warp never meet, whatever the weights' distribution (accumulated weights share few
 // exponents, equal ones are frequent).  The CTAs exchange their 256 sums through distributed shared
 // memory.  Two passes fix 16 bits of the threshold; where few keys share them (the usual case), one
@@ -15,18 +16,31 @@
 // the number of instructions a key and the cluster's barriers, not the 4 bytes a row.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace hisa {
 namespace {
 
 namespace cg = cooperative_groups;
+using tc::global_ns;
+using tc::kStatusTimeout;
+using tc::kWaitNs;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kClusters16 = 7;      // clusters of 16 CTAs of an SM each that run at a time
 constexpr int kStaged = 46 * 1024;  // keys a CTA holds in shared memory
 constexpr int kFew = 1024;          // keys of the cluster that are collected
+// A cooperative grid takes sequences from kWideRows rows on that get kMinWide CTAs or more, of kWidePart rows
+// at least.  Its barriers and the counters in global memory cost about 8 us more than a cluster's: 1 x 256K rows
+// 21.9 us against 20.3; 1 x 512K 24.6 against 28; 1 x 1M 31 against 47; 1 x 8M 69 against 415; 4 x 2M 52 against
+// 106.  With parts of 8192 rows 1 x 1M takes 39 us: the counters' atomics of 122 CTAs meet.
+constexpr int64_t kWideRows = 524288, kWidePart = 16384;
+constexpr int kMinWide = 16;
 
 struct alignas(16) Shared {
   uint32_t copies[256][32];  // counters of the running pass, copy = lane
@@ -55,22 +69,66 @@ __device__ __forceinline__ void count_if(bool hit, uint32_t counter) {
                : "memory");
 }
 
+// What the CTAs of one sequence share where they are no cluster.
+struct Global {
+  uint32_t totals[4][256];  // a pass's counters
+  uint32_t arrived;         // CTAs at the barriers so far
+  uint32_t counts[][2];     // [CTA] keys above and at the threshold
+};
+__host__ __device__ constexpr size_t global_bytes(int nc) { return sizeof(uint32_t) * (4 * 256 + 1 + 2 * (size_t)nc); }
+
+// WIDE: nc CTAs of a cooperative grid share a sequence, else a cluster.
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_keep_kernel(const float* __restrict__ weight, const int32_t* kv_len, int64_t n_kv, int budget, int n_first,
-                      int n_recent, int32_t* __restrict__ keep_idx, int32_t* kept_len, int32_t* __restrict__ status) {
+                      int n_recent, int32_t* __restrict__ keep_idx, int32_t* kept_len, int32_t* __restrict__ status,
+                      int nc, uint8_t* ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sm = *reinterpret_cast<Shared*>(smem);
   uint4* held = reinterpret_cast<uint4*>(smem + sizeof(Shared));
   cg::cluster_group cluster = cg::this_cluster();
-  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int rank = (int)blockIdx.x % nc;  // a cluster's CTAs follow one another
   const int64_t seq = blockIdx.x / nc;
+  Global* const global = WIDE ? reinterpret_cast<Global*>(ws + seq * global_bytes(nc)) : nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // A barrier of the sequence's CTAs.  A cooperative grid's CTAs are all there, so its wait ends; should one not
+  // come within a second, the others stop too.
+  uint32_t due = 0;
+  auto sync = [&]() {
+    if constexpr (WIDE) {
+      __shared__ int gone;
+      due += (uint32_t)nc;
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        atomicAdd(&global->arrived, 1u);
+        const uint64_t t0 = global_ns();
+        uint32_t n;
+        do {
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(&global->arrived) : "memory");
+        } while (n < due && global_ns() - t0 < kWaitNs);
+        gone = n < due;
+        if (gone && status) atomicOr(status, kStatusTimeout);
+      }
+      __syncthreads();
+      return gone == 0;
+    } else {
+      cluster.sync();
+      return true;
+    }
+  };
   int32_t* out = keep_idx + seq * budget;
   int64_t L = kv_len[seq];
   for (int i = tid; i < 256 * 32 / 4; i += kThreads) reinterpret_cast<uint4*>(sm.copies)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) sm.n_few = 0;
   if (tid < kWarps) sm.warp_gt[tid] = sm.warp_eq[tid] = 0;
-  cluster.sync();  // kept_len may be kv_len
+  if constexpr (WIDE) {
+    if (rank == 0) (&global->totals[0][0])[tid] = 0;
+    if (rank == 0 && tid == 0) global->arrived = 0;
+    cg::this_grid().sync();
+  } else {
+    cluster.sync();  // kept_len may be kv_len
+  }
   if (L < 0 || L > n_kv) {
     if (rank == 0 && tid == 0 && status) atomicOr(status, kStatusBadIndex);
     L = 0;
@@ -170,10 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int bin = warp * (256 / kWarps) + b;
       const uint32_t c = __reduce_add_sync(0xFFFFFFFFu, sm.copies[bin][lane]);
       sm.copies[bin][lane] = 0;
-      if (lane == 0) mine[bin] = c;
+      if (lane != 0) continue;
+      if (!WIDE)
+        mine[bin] = c;
+      else if (c != 0)
+        atomicAdd(&global->totals[pass][bin], c);
     }
-    cluster.sync();
-    if (tid < 256) {
+    if (!sync()) return;
+    if (WIDE) {
+      if (tid < 256) sm.totals[tid] = __ldcg(&global->totals[pass][tid]);
+    } else if (tid < 256) {
       uint32_t c[kMaxCluster];
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) c[r] = r < nc ? cluster.map_shared_rank(mine, r)[tid] : 0u;
@@ -292,23 +356,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t g = __reduce_add_sync(0xFFFFFFFFu, sm.warp_gt[lane]);
     const uint32_t e = __reduce_add_sync(0xFFFFFFFFu, sm.warp_eq[lane]);
     if (lane == 0) {
-      sm.counts[0] = g;
-      sm.counts[1] = e;
+      uint32_t* counts = WIDE ? global->counts[rank] : sm.counts;
+      counts[0] = g;
+      counts[1] = e;
     }
   }
-  cluster.sync();
+  if (!sync()) return;
   // keys above and at the threshold in front of this warp's range
   uint32_t above = 0, ties = 0;
-  if (lane < rank) {  // rank <= 15
-    const uint32_t* theirs = cluster.map_shared_rank(sm.counts, lane);
-    above = theirs[0];
-    ties = theirs[1];
+  for (int r = lane; r < rank; r += 32) {
+    if (WIDE) {
+      above += __ldcg(&global->counts[r][0]);
+      ties += __ldcg(&global->counts[r][1]);
+    } else {  // r <= 15
+      const uint32_t* theirs = cluster.map_shared_rank(sm.counts, r);
+      above = theirs[0];
+      ties = theirs[1];
+    }
   }
   above += lane < warp ? sm.warp_gt[lane] : 0u;
   ties += lane < warp ? sm.warp_eq[lane] : 0u;
   above = __reduce_add_sync(0xFFFFFFFFu, above);
   ties = __reduce_add_sync(0xFFFFFFFFu, ties);
-  cluster.sync();  // no CTA leaves while its counts are read
+  if (!WIDE) cluster.sync();  // no CTA leaves while its counts are read
   const uint32_t quota = tie ? krem : 0xFFFFFFFFu;
   uint32_t place = n_first + above + min(ties, quota);
   const uint32_t below = (1u << lane) - 1u;
@@ -362,38 +432,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// CTAs of a cooperative grid per sequence, or 0 where a cluster takes it.
+int wide_ctas(const Shape& s) {
+  const int64_t nc = std::min<int64_t>(148 / s.batch, s.n_kv / kWidePart);
+  return s.n_kv >= kWideRows && nc >= kMinWide ? (int)nc : 0;
+}
+
 }  // namespace
 
-size_t cache_keep_workspace_bytes(const Shape&) { return 0; }
+size_t cache_keep_workspace_bytes(const Shape& s) {
+  const int nc = wide_ctas(s);
+  return nc > 0 ? (size_t)s.batch * global_bytes(nc) : 0;
+}
 
 cudaError_t launch_cache_keep(const Shape& s, const float* weight, const int32_t* kv_len, int budget, int n_first,
-                              int n_recent, int32_t* keep_idx, int32_t* kept_len, int32_t* status, void*,
+                              int n_recent, int32_t* keep_idx, int32_t* kept_len, int32_t* status, void* ws,
                               cudaStream_t st) {
-  // CTAs per sequence: as many as leave every CTA 4096 rows or more while the call stays on one wave
-  // of the 148 SMs.
-  int nc = 1;
-  while (nc < kMaxCluster && (int64_t)s.batch * nc * 2 <= 148 && s.n_kv >= (int64_t)nc * 2 * 4096) nc *= 2;
+  const int wide = wide_ctas(s);
+  int nc = wide;
+  if (wide == 0) {
+    // Clusters: as many CTAs as leave every one 4096 rows or more while the call stays on one wave of the SMs
+    // (1 x 16K rows: 12.6 us with 4 CTAs, 16.1 with one; 8 x 64K: 14.4 with 8); 16 only for 8192 rows each and
+    // where so many clusters run at a time (6 x 64K: 17.1 us with 16, 15.1 with 8; 6 x 256K: 21 and 25;
+    // 8 x 256K: 34 in two waves, 25 with 8).
+    nc = 1;
+    while (nc < kMaxCluster / 2 && (int64_t)s.batch * nc * 2 <= 148 && s.n_kv >= (int64_t)nc * 2 * 4096) nc *= 2;
+    if (nc == kMaxCluster / 2 && s.batch <= kClusters16 && s.n_kv >= kMaxCluster * 8192) nc = kMaxCluster;
+  }
   const int64_t part = (s.n_kv + 3 + nc - 1) / nc + 4;  // keys of a part at the most: whole groups of four
   const size_t smem = sizeof(Shared) + 4 * (size_t)(part < kStaged ? (part + 3) / 4 * 4 : kStaged);
-  cudaError_t e = ensure_smem((const void*)cache_keep_kernel, (int)(sizeof(Shared) + 4 * (size_t)kStaged));
+  const auto kern = wide > 0 ? cache_keep_kernel<true> : cache_keep_kernel<false>;
+  cudaError_t e = ensure_smem((const void*)kern, (int)(sizeof(Shared) + 4 * (size_t)kStaged));
   if (e != cudaSuccess) return e;
-  if (nc > 8) {
-    e = cudaFuncSetAttribute(cache_keep_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  if (wide > 0) {
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+  } else {
+    if (nc > 8) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)nc;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(s.batch * nc));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)nc;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_keep_kernel, weight, kv_len, s.n_kv, budget, n_first, n_recent, keep_idx,
-                            kept_len, status);
+  return cudaLaunchKernelEx(&cfg, kern, weight, kv_len, s.n_kv, budget, n_first, n_recent, keep_idx, kept_len, status,
+                            nc, static_cast<uint8_t*>(ws));
 }
 
 }  // namespace hisa

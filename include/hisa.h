@@ -372,7 +372,9 @@ hisa_status_t hisa_tree_attn_fwd(const hisa_params_t* params, const void* q, con
  * *dev_status); NULL counts every slot.  A row of lse that is -inf counts
  * nothing.  Only K is read, once for all counted slots.  A prompt's last
  * tokens are a chain of T slots behind the first n - T rows.  The sums are
- * formed in a fixed order: equal inputs give equal bits. */
+ * formed in a fixed order: equal inputs give equal bits.  Workspace:
+ * hisa_cache_weight_workspace_size bytes, 16-byte aligned, used by one call at a
+ * time. */
 hisa_status_t hisa_cache_weight_workspace_size(const hisa_params_t* params, size_t* bytes);
 hisa_status_t hisa_cache_weight(const hisa_params_t* params, const void* q, const void* k, const int32_t* kv_len,
                                 const int32_t* parent, const int32_t* path, const float* lse, float* weight,
@@ -386,7 +388,8 @@ hisa_status_t hisa_cache_weight(const hisa_params_t* params, const void* q, cons
  * min(L, budget) (may be kv_len itself).  0 <= L <= n_kv, else the list
  * is all -1, kept_len 0 and bit 0 of *dev_status is set.  budget in [1, n_kv],
  * n_first, n_recent >= 0, n_first + n_recent <= budget.  Uses batch and n_kv of
- * params. */
+ * params.  Workspace: hisa_cache_keep_workspace_size bytes (0 but for a few long
+ * sequences), 16-byte aligned, used by one call at a time. */
 hisa_status_t hisa_cache_keep_workspace_size(const hisa_params_t* params, size_t* bytes);
 hisa_status_t hisa_cache_keep(const hisa_params_t* params, const float* weight, const int32_t* kv_len, int32_t budget,
                               int32_t n_first, int32_t n_recent, int32_t* keep_idx, int32_t* kept_len,

@@ -433,6 +433,55 @@ def test_kept_rows_of_one_long_cache_and_many_short_ones(hs):
     check_keep(hs, torch.rand(500, 400, generator=gen), lens, 64, 4, 16)
 
 
+@pytest.mark.parametrize("b", [1, 3, 4])
+def test_kept_rows_of_a_few_long_caches(hs, b):
+    """Sequences that finish at different steps of the selection side by side: ties down to the last bit, equal
+    weights, a threshold in the first digit, lengths below the budget, out of range and of zero."""
+    gen = torch.Generator().manual_seed(b)
+    n_kv = 540_001
+    w = torch.rand(b, n_kv, generator=gen)
+    w[0] = (w[0] * 50).floor() + 2.0**-10 * (w[0] < 0.3)
+    w[-1, 1000:200_000] = 0.25
+    for lens in ([n_kv] * b, [n_kv - 1, 70_000, 0, n_kv][:b], [n_kv + 1, n_kv, -1, 262_144][:b], [524_289] * b):
+        for budget, first, recent in ((70_001, 3, 1000), (1, 0, 0), (50, 20, 30), (n_kv - 2, 1, 1)):
+            check_keep(hs, w, lens, budget, first, recent, alias=budget == 70_001)
+    w[0, :135_000], w[0, 135_000:] = 1.0, 2.0**40  # the first digit decides
+    check_keep(hs, w, [n_kv] * b, n_kv - 135_000)
+
+
+def test_long_caches_on_two_streams(hs):
+    """Choices over long caches on two streams at once, and one captured and replayed: as one after the other."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    n_kv, budget = 600_000, 9_000
+    p = hs.params(2, 1, n_kv, 128, 128, 4, 64)
+    w = [torch.rand(2, n_kv, generator=gen, device="cuda") for _ in range(4)]
+    lens = torch.tensor([n_kv, 560_001], dtype=torch.int32, device="cuda")
+
+    def choose(x, stream=None):
+        idx = torch.empty(2, budget, dtype=torch.int32, device="cuda")
+        kept = torch.empty(2, dtype=torch.int32, device="cuda")
+        torch.cuda.current_stream().synchronize()
+        for _ in range(5):
+            hs.hisa_cache_keep(p, x, lens, budget, idx, kept, 1, 7, stream=stream)
+        return idx, kept
+
+    want = [choose(x) for x in w]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [choose(x, streams[i % 2]) for i, x in enumerate(w)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x, idx, kept = w[0].clone(), torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hs.hisa_cache_keep(p, x, lens, budget, idx, kept, 1, 7)
+    for y, z in zip(w, want):
+        x.copy_(y)
+        graph.replay()
+        assert torch.equal(idx, z[0]) and torch.equal(kept, z[1])
+
+
 def test_bad_lengths_keep_nothing(hs):
     check_keep(hs, torch.rand(3, 100), [-1, 50, 101], 20)
 
