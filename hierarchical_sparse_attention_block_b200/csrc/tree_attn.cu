@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kWeighThreads)
 int row_tiles(const Shape& s) { return s.n_q * (s.H / s.Hkv) > kRows ? 2 : 1; }
 
 // With few query rows the weights come from kept scores: writing and reading those moves 8 bytes a query
-// row and key, reading K again 2 d bytes a KV head and key (8 x 64K rows, one query row a KV head: 500 us
+// row and key, reading K again 2 d bytes a KV head and key (8 x 64K rows, one query row a KV head: 490 us
 // this way, 740 with K read again).
 bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kFewRows; }
 int64_t score_stride(const Shape& s) { return (s.n_kv + kRows - 1) / kRows * kRows; }

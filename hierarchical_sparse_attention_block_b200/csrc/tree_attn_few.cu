@@ -4,7 +4,7 @@
 //   S^T = K Q^T  (128 keys x N),   O^T += V^T P^T  (D x N),   N = 16 >= T H / Hk query rows.
 //
 // The call is bound by the cache's bytes (K and V once): 8 x 64K rows, one query row a KV head, take
-// 432 us, 6.7 TB/s.  With the query rows as the M = 128 of the products, as tree_attn.cu has them, one to
+// 421 us, 6.8 TB/s.  With the query rows as the M = 128 of the products, as tree_attn.cu has them, one to
 // 16 of 128 rows would be padding (446 us, with weights of 8 bits).  Here the products shrink with N, a
 // thread, which owns a key, forms that key's weights of all rows, and keeping the scores for the weights
 // that the rows receive is a coalesced store.  From 17 rows on the stores of the weights, two bytes at a
@@ -14,7 +14,8 @@
 // Work and ring buffers are those of tree_attn.cu (one row tile).  Scores and weights have two buffers,
 // used by the key tiles in turn; the two softmax groups of four warps take half of the query rows each.
 // A row's softmax runs over the lanes here.  Its reference max is one number for the group's warps; it
-// moves, for all of them, when a score exceeds it by 2^8: each tile the warps look for that while they
+// starts as the first key's score and moves, for all of them, when a score exceeds it by 2^8: each tile the
+// warps look for that while they
 // form the weights (no reduction over lanes), agree at a barrier, and only where one found it, rarely,
 // reduce the rows' max, rescale and form the weights again.  A row's sum stays a partial sum per thread
 // until the segment's end.  The weights go to shared memory, in the layout of the second product's
@@ -321,6 +322,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j >= T || !sees(tree, parent != nullptr, slots[row0 + i], j)) s[i] = 0xFF800000u;
           }
         };
+        if (x == 0) {
+          // A reference to start from: the score of the segment's first key, where the row sees it.
+          if ((warp & 3) == 0) {
+            uint32_t s[NR];
+            load(s);
+            if (lane == 0) {
+#pragma unroll
+              for (int i = 0; i < NR; ++i) {
+                const float z = __uint_as_float(s[i]) * qscale;
+                if (z > -INFINITY && z < INFINITY) rows[i] = make_float2(z, 8.f);
+              }
+            }
+          }
+          agree();
+          if (!ok) break;
+        }
         float p[NR];
         while (true) {
           bool up = false;
@@ -418,13 +435,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       // the rows' sums: over the lanes, then over the warps
-      float mine = 0.f;
+      // (half of the rows change lanes at each step: lane 4 i ends with row i)
+      static_assert(NR == 8, "three halvings leave one row a lane");
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float sum = warp_sum(l[i]);
-        if (lane == i) mine = sum;
+      for (int h = NR / 2; h >= 1; h /= 2) {
+        const bool upper = (lane & (4 * h)) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i)
+          l[i] = (upper ? l[i + h] : l[i]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? l[i] : l[i + h], 4 * h);
       }
-      if (lane < NR) per_warp[(warp & 3) * N + lane] = mine;
+      l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 2);
+      l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], 1);
+      if ((lane & 3) == 0) per_warp[(warp & 3) * N + lane / 4] = l[0];
       agree();
       if (!ok) break;
       if (r < NR) {
@@ -437,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = INFINITY;
         }
         join[r] = make_float2(m, sum);
+        alphas[r] = sum == 0.f ? 0.f : 1.f / sum;
       }
       agree();
       if (!ok) break;
@@ -448,27 +471,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       tmem_ld<NR>(to, ov);
       if (r < D) {
+        float y[NR];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const int row = row0 + i;
-          if (row >= R) continue;
-          const float sum = join[i].y;
-          float y = sum == 0.f ? 0.f : __uint_as_float(ov[i]);
-          const int slot = slots[row];
-          if (any_odd && !(treed && tree.end[slot] != kRoot)) {
-            // values that are not finite, of the rows this token sees in this segment
+        for (int i = 0; i < NR; ++i) y[i] = join[i].y == 0.f ? 0.f : __uint_as_float(ov[i]);
+        if (any_odd) {
+          // values that are not finite, of the rows that a token sees in this segment
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int slot = slots[row0 + i];
+            if (row0 + i >= R || (treed && tree.end[slot] != kRoot)) continue;
             for (int jj = 0; jj < T; ++jj) {
               if (!((odd[jj >> 5] >> (jj & 31)) & 1u) || !sees(tree, parent != nullptr, slot, jj)) continue;
               const uint32_t b = args.v[((seq * n_kv + L + jj) * Hkv + g) * D + r];
-              if ((b & 0x7F80u) == 0x7F80u) y += bf16_lo(b);
+              if ((b & 0x7F80u) == 0x7F80u) y[i] += bf16_lo(b);
             }
           }
-          if (whole) {
-            const int64_t to_row = (seq * T + slot) * H + g * G + (row - slot * G);
-            reinterpret_cast<__nv_bfloat16*>(args.o)[to_row * D + r] = __float2bfloat16_rn(sum == 0.f ? y : y / sum);
-          } else {
-            reinterpret_cast<float*>(args.work.part_o + (part * (D / 4) + r / 4) * N + row)[r & 3] = y;
+        }
+        if (whole) {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.o) + (seq * T * H + g * G) * D + r;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int row = row0 + i, slot = slots[row];
+            if (row < R)
+              o[((int64_t)slot * H + (row - slot * G)) * D] =
+                  __float2bfloat16_rn(join[i].y == 0.f ? y[i] : y[i] * alphas[i]);
           }
+        } else {
+          float* o = reinterpret_cast<float*>(args.work.part_o + (part * (D / 4) + r / 4) * N + row0) + (r & 3);
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            if (row0 + i < R) o[4 * i] = y[i];
         }
       }
       __syncwarp();
