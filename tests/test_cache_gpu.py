@@ -449,6 +449,14 @@ def test_kept_rows_of_a_few_long_caches(hs, b):
     check_keep(hs, w, [n_kv] * b, n_kv - 135_000)
 
 
+@pytest.mark.parametrize("b,n_kv", [(1, 7_900_001), (9, 800_003), (10, 400_001), (60, 110_003)])
+def test_kept_rows_of_parts_beyond_shared_memory(hs, b, n_kv):
+    gen = torch.Generator().manual_seed(n_kv)
+    w = torch.rand(b, n_kv, generator=gen)
+    w[-1] = (w[-1] * 300).floor()
+    check_keep(hs, w, [n_kv - 5 * s for s in range(b)], 20_000, 5, 600)
+
+
 def test_long_caches_on_two_streams(hs):
     """Choices over long caches on two streams at once, and one captured and replayed: as one after the other."""
     gen = torch.Generator(device="cuda").manual_seed(5)
@@ -648,6 +656,19 @@ def test_a_refused_eviction_changes_nothing(hs):
         hs.evict(p, weight, kv_len, 0, [k])
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(before, (k, weight, kv_len)))
+
+
+@pytest.mark.parametrize("first", [-300.0, -20.0, 20.0, 300.0])
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_a_first_key_far_from_the_others(hs, first, T):
+    """Every segment of keys starts with a score far above or below the rest, both for some rows."""
+    H, Hk, d = 4, 2, 64
+    x = make_inputs(3, T, H, Hk, d, 700, [660, 3, 128], "tree", seed=T)
+    for t in range(0, 128 * 5, 128):
+        for s, L in enumerate((660, 3, 128)):
+            if t < L:
+                x["k"][s, t] = (first * x["q"][s, 0, ::H // Hk].float()).to(torch.bfloat16)
+    check_tree(hs, x, H, Hk, d, True)
 
 
 @pytest.mark.parametrize("T,H", [(15, 1), (16, 1), (17, 1), (127, 1), (128, 1), (129, 1), (64, 4), (129, 2)])
