@@ -143,11 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t policy = l2_evict_first();  // K and V pass through the L2 once
       int slot = 0, issued = 0;
       uint32_t phase = 1;  // parity of the slot's last release
-      // The query rows go first: behind the first tiles of every SM they would wait for all of those.
-      bool ok = walk.u >= walk.u1 || mbar_wait_or_abort(bar(C::B_GO), 0, abort_flag);
+      bool ok = true;
       while (ok && walk.next()) {
         for (int x = 0; x < walk.n; ++x) {
-          if (issued >= NS && !mbar_wait_or_abort(bar(empty + slot), phase, abort_flag)) {
+          // The query rows go first: behind the first tiles of every SM they would wait for all of those.  (A CTA
+          // whose units hold no tile has none, and asks for none.)
+          if ((issued == 0 && !mbar_wait_or_abort(bar(C::B_GO), 0, abort_flag)) ||
+              (issued >= NS && !mbar_wait_or_abort(bar(empty + slot), phase, abort_flag))) {
             fail();
             ok = false;
             break;

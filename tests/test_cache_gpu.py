@@ -658,6 +658,13 @@ def test_a_refused_eviction_changes_nothing(hs):
     assert all(torch.equal(x, y) for x, y in zip(before, (k, weight, kv_len)))
 
 
+@pytest.mark.parametrize("T,H,rows", [(20, 1, 95_300), (100, 2, 95_300), (100, 2, 96_700), (3, 1, 95_300)])
+def test_five_tiles_for_every_sm(hs, T, H, rows):
+    """One item over the whole GPU: the first share of the work may hold no key tile at all."""
+    x = make_inputs(1, T, H, 1, 64, rows + T, [rows], "tree", seed=T, garbage=False)
+    check_tree(hs, x, H, 1, 64, True)
+
+
 @pytest.mark.parametrize("first", [-300.0, -20.0, 20.0, 300.0])
 @pytest.mark.parametrize("T", [1, 5, 40])
 def test_a_first_key_far_from_the_others(hs, first, T):
