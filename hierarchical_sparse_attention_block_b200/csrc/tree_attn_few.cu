@@ -16,13 +16,15 @@
 // A row's softmax runs over the lanes here.  Its reference max is one number for the group's warps; it
 // starts as the score of the segment's first key and moves, for all of them, when a score exceeds it by
 // 2^8: each tile the warps look for that while they form the weights (no reduction over lanes), agree at a
-// barrier, and only where one found it, rarely, reduce the rows' max, rescale and form the weights again.
+// barrier, and only where one found it, rarely, reduce the rows' max, rescale and form the weights again (once a
+// tile: after that no score of the tile exceeds it; row_ref.h has the arithmetic).
 // (Starting from the first tile's max instead: 1 x 1K rows, 16 query rows, 18.2 us, 15.7 this way with the
 // sums by halving.)  A row's sum stays a partial sum per thread until the segment's end.  The weights go to shared memory, in the layout of the second product's
 // operand, as two bf16 numbers each (16 significant bits).
 // Every wait is bounded (1 s): a timeout sets status bit 1 and the CTA stops.
 #include <math.h>
 
+#include "row_ref.h"
 #include "tree_attn.cuh"
 
 namespace hisa {
@@ -50,7 +52,7 @@ struct Cfg {
   static constexpr int K_OFF = 0, V_OFF = K_OFF + KS * kTile, P_OFF = V_OFF + VS * kTile;
   static constexpr int Q_OFF = P_OFF + 4 * kWeights;  // weight buffer b, part p at P_OFF + (2 b + p) * kWeights
   static constexpr int TREE_OFF = Q_OFF + kQHalf * (D / 64);
-  static constexpr int ROW_OFF = TREE_OFF + (int)sizeof(DraftTree);     // float2 [N]: reference max, threshold
+  static constexpr int ROW_OFF = TREE_OFF + (int)sizeof(DraftTree);     // RowRef [N]
   static constexpr int ALPHA_OFF = ROW_OFF + N * (int)sizeof(float2);    // float [N]
   static constexpr int MAX_OFF = ALPHA_OFF + N * 4;                      // float [4][N]: per warp; then the sums
   static constexpr int JOIN_OFF = MAX_OFF + 4 * N * 4;                   // float2 [N]: max, sum
@@ -249,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid & (kRows - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t to = tmem + lanes + 128u + (uint32_t)row0;
-    float2* rows = reinterpret_cast<float2*>(smem + C::ROW_OFF) + row0;
+    RowRef* rows = reinterpret_cast<RowRef*>(smem + C::ROW_OFF) + row0;
+    const float limit = rise_limit(qscale);
     float* alphas = reinterpret_cast<float*>(smem + C::ALPHA_OFF) + row0;
     float* per_warp = reinterpret_cast<float*>(smem + C::MAX_OFF) + row0;  // [4] at pitch N
     float2* join = reinterpret_cast<float2*>(smem + C::JOIN_OFF) + row0;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_arrive(bar(C::B_QFULL));
       if (tid < kDraftWords) odd_rows[((seg + 1) & 1) * kDraftWords + tid] = 0u;
-      if (r < NR) rows[r] = make_float2(0.f, -INFINITY);  // no score yet: any raises
+      if (r < NR) rows[r] = {0.f, -INFINITY};
       uint32_t* odd = odd_rows + (seg & 1) * kDraftWords;
       const bool treed = parent && (walk.j0 + walk.n) * kRows > L;  // the segment reaches behind the context
       if (treed) {
@@ -332,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
 #pragma unroll
               for (int i = 0; i < NR; ++i) {
-                const float z = __uint_as_float(s[i]) * qscale;
-                if (z > -INFINITY && z < INFINITY) rows[i] = make_float2(z, 8.f);
+                const float z = __uint_as_float(s[i]);
+                if (z > -INFINITY && z < INFINITY) rows[i] = {z, limit};
               }
             }
           }
@@ -341,11 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         float p[NR];
-        while (true) {
+        // The weights; formed a second time, and for good, if a score asks for another reference.
+        for (bool raised = false;; raised = true) {
           bool up = false;
           uint32_t s[NR];
           load(s);
-          if (scores) {
+          if (scores && !raised) {
 #pragma unroll
             for (int i = 0; i < NR; ++i)
               if (row0 + i < R) scores[i * args.score_stride + t0] = __uint_as_float(s[i]) * qscale;
@@ -353,13 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < NR; i += 2) {
             const float4 st = *reinterpret_cast<const float4*>(rows + i);
-            const float x0 = fmaf(__uint_as_float(s[i]), qscale, -st.x);
-            const float x1 = fmaf(__uint_as_float(s[i + 1]), qscale, -st.z);
-            up |= x0 > st.y;
-            up |= x1 > st.w;
-            p[i] = fast_exp2(x0);  // 0 where masked
-            p[i + 1] = fast_exp2(x1);
+            const RowRef r0 = {st.x, st.y}, r1 = {st.z, st.w};
+            const float s0 = __uint_as_float(s[i]), s1 = __uint_as_float(s[i + 1]);
+            up |= exceeds(s0, r0);
+            up |= exceeds(s1, r1);
+            p[i] = fast_exp2(exponent(s0, r0, qscale));  // 0 where masked
+            p[i + 1] = fast_exp2(exponent(s1, r1, qscale));
           }
+          if (raised) break;
           if (__any_sync(0xFFFFFFFFu, up) && lane == 0) raise_flag[t] = 1;
           agree();
           if (!ok || !raise_flag[t]) break;
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mine = -INFINITY;
 #pragma unroll
           for (int i = 0; i < NR; ++i) {
-            const float top = warp_max(__uint_as_float(s[i]) * qscale);
+            const float top = warp_max(__uint_as_float(s[i]));
             if (lane == i) mine = top;
           }
           if (lane < NR) per_warp[(warp & 3) * N + lane] = mine;
@@ -375,14 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (r == 0) raise_flag[t] = 0;
           if (r < NR) {
-            const float2 st = rows[r];
+            const RowRef st = rows[r];
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < 4; ++w) top = fmaxf(top, per_warp[w * N + r]);
             float alpha = 1.f;
-            if (top - st.x > st.y) {
-              alpha = st.y == -INFINITY ? 1.f : exp2f(st.x - top);  // no score yet: nothing to rescale
-              rows[r] = make_float2(top, 8.f);
+            if (exceeds(top, st)) {
+              const RowRef moved = {top, limit};
+              if (st.limit != -INFINITY) alpha = exp2f(exponent(st.ref, moved, qscale));  // else nothing to rescale
+              rows[r] = moved;
             }
             alphas[r] = alpha;
           }
@@ -452,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       agree();
       if (!ok) break;
       if (r < NR) {
-        const float2 st = rows[r];
-        float m = st.y == -INFINITY ? -INFINITY : st.x;
+        const RowRef st = rows[r];
+        float m = st.limit == -INFINITY ? -INFINITY : st.ref * qscale;  // log2 domain
         float sum = (per_warp[r] + per_warp[N + r]) + (per_warp[2 * N + r] + per_warp[3 * N + r]);
         // an empty slot; where the segment ends within the context, the merge learns it from another part
         if (treed && tree.end[slots[row0 + r]] != kRoot) {

@@ -1,0 +1,85 @@
+"""The cache operators at the edges of their arithmetic and of their orderings, against the definitions in 64 bits
+(tolerances: test_cache_gpu.py, unless a test derives its own)."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import cache_reference as ref  # noqa: E402
+from row_ref_cases import limit_of, next_to_the_limit, qscale_of, three_bf16  # noqa: E402
+from test_cache_gpu import check_tree, close, hs, make_inputs, to_gpu  # noqa: E402, F401
+
+
+def scores_next_to_the_limit(T, H, b, n_kv, d, seed):
+    """One KV head whose raw scores are chosen to the last bit: q is 1 in three places, a key holds its score as three
+    bf16 numbers there.  Every tile's largest score lies 8 (log2 domain) above the one before, give or take an ulp."""
+    q_scale = qscale_of(d)
+    rng = np.random.default_rng(seed)
+    x = make_inputs(b, T, H, 1, d, n_kv, [n_kv - T - s % 3 for s in range(b)], "chain", seed, garbage=False)
+    x["q"].zero_()
+    x["q"][..., :3] = 1.0
+    for s, (first, up) in enumerate(next_to_the_limit(q_scale, b, seed)):
+        z = (first - np.float32(3) * limit_of(q_scale) * rng.random(n_kv, dtype=np.float32)).astype(np.float32)
+        top = first
+        for t0 in range(0, n_kv, 128):
+            z[t0] = first
+            if t0 == 0:
+                top = up
+            else:
+                top = np.float32(top + limit_of(q_scale))
+                for _ in range(rng.integers(0, 3)):
+                    top = np.nextafter(top, np.float32(rng.choice([-np.inf, np.inf])))
+            z[t0 + 1 + rng.integers(0, min(127, n_kv - t0 - 1))] = top
+        for c, part in enumerate(three_bf16(z)):
+            x["k"][s, :, 0, c] = torch.from_numpy(part).to(torch.bfloat16)
+    return x
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 2), (16, 1)])
+def test_scores_next_to_the_raise_of_the_reference(hs, T, H):
+    x = scores_next_to_the_limit(T, H, 150, 700, 64, seed=T)
+    check_tree(hs, x, H, 1, 64, True)
+
+
+def far_scores(T, H, Hk, d, n_kv, L, size, seed):
+    """Keys along one direction, at a few lengths that double: a row's largest scores are about +size, equal among
+    themselves to the last bit, all others at most half as large; the rows of odd slots look the other way."""
+    x = make_inputs(1, T, H, Hk, d, n_kv, [L], "tree", seed, garbage=False)
+    gen = torch.Generator().manual_seed(seed + 1)
+    u = torch.randn(d, generator=gen).to(torch.bfloat16).float()
+    e = math.log2(size * math.sqrt(d) / float((u * u).sum()))
+    a, c = int(e / 2), int(e) - int(e / 2)
+    level = 2.0 ** torch.randint(-6, 0, (n_kv,), generator=gen).float()
+    level = torch.where(torch.rand(n_kv, generator=gen) < 0.5, level, -level)
+    tops = torch.randperm(L, generator=gen)[:24]
+    level[tops[:12]], level[tops[12:]] = 1.0, -1.0
+    sign = 1.0 - 2.0 * (torch.arange(T) % 2)
+    x["q"] = (u * 2.0**a * sign[:, None, None]).expand(1, T, H, d).to(torch.bfloat16).contiguous()
+    x["k"] = (u * 2.0**c * level[None, :, None, None]).expand(1, n_kv, Hk, d).to(torch.bfloat16).contiguous()
+    return x
+
+
+def check_far(hs, size, T, H, Hk, d, n_kv, L):
+    """A score is off by (d + 8) 2^-23 of itself, 2e-5 of the distance of at least half to any other score, so the
+    weights are those of the largest scores alone, and these are equal: o carries the roundings of the weights (equal
+    ones cancel, 2^-14 for the sums) and of the output, lse the largest score's error."""
+    x = far_scores(T, H, Hk, d, n_kv, L, size, seed=int(math.log2(size)) + T)
+    p = hs.params(1, T, n_kv, 128, 128, 4, 64, H, Hk, d)
+    g = to_gpu(x)
+    o, lse = hs.tree_attn(p, g["q"], g["k"], g["v"], g["kv_len"], parent=g["parent"])
+    ro, rl, _, spread, _ = ref.tree_attention(x["q"], x["k"], x["v"], x["kv_len"], x["parent"], 1 / math.sqrt(d))
+    assert float(rl.min()) > size / 4
+    close(o, ro, 2.0**-8 * ro.abs() + 2.0**-13 * spread, "o")
+    close(lse, rl, (d + 8) * 2.0**-23 * rl + 2.0**-22 * rl, "lse")
+
+
+SIZES = [2.0**24, 2.0**27, 2.0**28, 2.0**31, 2.0**34, 1e12, 2.0**70, 2.0**100]
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("T,H,Hk,d", [(2, 2, 2, 64), (8, 4, 2, 128)])
+def test_large_finite_scores(hs, size, T, H, Hk, d):
+    check_far(hs, size, T, H, Hk, d, 2000, 1900)
