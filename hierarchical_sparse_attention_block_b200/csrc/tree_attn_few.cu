@@ -75,7 +75,7 @@ struct Cfg {
   };
   static constexpr int WALK_OFF = BAR_OFF + kNBar * 8;
   static constexpr int MISC_OFF = WALK_OFF + (int)sizeof(WalkShared<kThreads>);
-  static constexpr int kSmem = MISC_OFF + 4 * (4 + 2 * kDraftWords) + 1024;  // + slack for the 1024-byte alignment
+  static constexpr int kSmem = MISC_OFF + 4 * (6 + 2 * kDraftWords) + 1024;  // + slack for the 1024-byte alignment
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && kQHalf % 1024 == 0, "swizzle atoms stay 1024-byte aligned");
   static_assert(P_OFF - V_OFF >= kTile && 4 * kWeights >= kHalf, "what lies behind a V tile is this block's memory");
@@ -101,8 +101,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* raise_flag = reinterpret_cast<volatile int*>(misc + 2);  // [2]: a row of the group exceeds its max
-  uint32_t* odd_rows = misc + 4;  // [2][kDraftWords] by segment parity: drafted V rows not all finite
+  // [2][2] by group and key tile parity: a row of the group exceeds its reference.  A warp may be a tile ahead of the
+  // others: past a tile's barrier, it waits for none of them until the next tile's.
+  volatile int* raise_flags = reinterpret_cast<volatile int*>(misc + 2);
+  uint32_t* odd_rows = misc + 6;  // [2][kDraftWords] by segment parity: drafted V rows not all finite
   auto fail = [&]() {
     *abort_flag = 1;
     if (status) atomicOr(status, kStatusTimeout);
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), group ? kRows : all || i == C::B_SYNC || i == C::B_QFULL || i == C::B_GO ? kSoftmax : 1);
     }
     *abort_flag = 0;
-    raise_flag[0] = raise_flag[1] = 0;
+    for (int i = 0; i < 4; ++i) raise_flags[i] = 0;
     mbar_init_fence();
   }
   if (tid < 2 * kDraftWords) odd_rows[tid] = 0u;
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < walk.n; ++x, ++cnt) {
         const int t0 = (walk.j0 + x) * kRows, buf = cnt & 1;
         const uint32_t ts = tmem + lanes + 64u * (uint32_t)buf + (uint32_t)row0;
+        volatile int* raise = raise_flags + 2 * t + buf;
         const bool tail = t0 + kRows > L;
         const int j = t0 + r - L;  // drafted row of this key, from the context's end on
         if (t == 0 && x == ahead_at) prefetch_next<D>(walk, args, 1, kFewRows, r);
@@ -365,9 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[i + 1] = fast_exp2(exponent(s1, r1, qscale));
           }
           if (raised) break;
-          if (__any_sync(0xFFFFFFFFu, up) && lane == 0) raise_flag[t] = 1;
+          if (__any_sync(0xFFFFFFFFu, up) && lane == 0) *raise = 1;
           agree();
-          if (!ok || !raise_flag[t]) break;
+          if (!ok || !*raise) break;
           // the rows' max over the tile, per warp and then over the warps
           float mine = -INFINITY;
 #pragma unroll
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < NR) per_warp[(warp & 3) * N + lane] = mine;
           agree();
           if (!ok) break;
-          if (r == 0) raise_flag[t] = 0;
+          if (r == 0) *raise = 0;
           if (r < NR) {
             const RowRef st = rows[r];
             float top = -INFINITY;

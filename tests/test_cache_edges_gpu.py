@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 import cache_reference as ref  # noqa: E402
 from row_ref_cases import limit_of, next_to_the_limit, qscale_of, three_bf16  # noqa: E402
-from test_cache_gpu import check_tree, close, hs, make_inputs, to_gpu  # noqa: E402, F401
+from test_cache_gpu import check_tree, close, delta, hs, make_inputs, to_gpu  # noqa: E402, F401
 
 
 def scores_next_to_the_limit(T, H, b, n_kv, d, seed):
@@ -42,6 +42,43 @@ def scores_next_to_the_limit(T, H, b, n_kv, d, seed):
 def test_scores_next_to_the_raise_of_the_reference(hs, T, H):
     x = scores_next_to_the_limit(T, H, 150, 700, 64, seed=T)
     check_tree(hs, x, H, 1, 64, True)
+
+
+def rising_keys(b, Hk, d, n_kv, seed):
+    """K whose raw scores against q = (1, 1, 1, 0 ..) rise by about the limit from tile to tile, at one key a tile."""
+    rng = np.random.default_rng(seed)
+    lim = limit_of(qscale_of(d))
+    tiles = -(-n_kv // 128)
+    top = np.cumsum(lim * rng.choice([0.0, 0.7, 1.0, 1.3], (b, Hk, tiles)), 2)
+    z = np.repeat(top, 128, 2)[:, :, :n_kv] - lim * rng.uniform(1, 3, (b, Hk, n_kv))
+    at = np.minimum(np.arange(tiles) * 128 + rng.integers(0, 128, (b, Hk, tiles)), n_kv - 1)
+    np.put_along_axis(z, at, top, 2)
+    k = torch.zeros(b, n_kv, Hk, d, dtype=torch.bfloat16)
+    for c, part in enumerate(three_bf16(z.transpose(0, 2, 1).astype(np.float32))):
+        k[..., c] = torch.from_numpy(part).to(torch.bfloat16)
+    return k
+
+
+@pytest.mark.parametrize("Hk,G,T", [(16, 1, 1), (4, 2, 8)])
+def test_references_that_move_from_tile_to_tile(hs, Hk, G, T):
+    """Dozens of tiles a share of the work, most of which move the reference, at a key of any warp: the definition's
+    result, and the same bits every time."""
+    b, d, n_kv = 2, 128, 24000
+    H = Hk * G
+    gen = torch.Generator().manual_seed(T)
+    k, v = rising_keys(b, Hk, d, n_kv, T), torch.randn(b, n_kv, Hk, d, generator=gen).to(torch.bfloat16)
+    q = torch.zeros(b, T, H, d, dtype=torch.bfloat16)
+    q[..., :3] = 1.0
+    lens = torch.tensor([n_kv - T, 17003], dtype=torch.int32)
+    ro, rl, _, spread, size = ref.tree_attention(q, k, v, lens, None, 1 / math.sqrt(d))
+    p = hs.params(b, T, n_kv, 128, 128, 4, 64, H, Hk, d)
+    g = [x.cuda() for x in (q, k, v, lens)]
+    first = hs.tree_attn(p, *g)
+    dl = delta(d, size)
+    close(first[1], rl, dl + 2.0**-22 * rl.abs(), "lse")
+    close(first[0], ro, 2.0**-8 * ro.abs() + 2 * dl * spread, "o")
+    for _ in range(40):
+        assert all(torch.equal(x, y) for x, y in zip(first, hs.tree_attn(p, *g)))
 
 
 def far_scores(T, H, Hk, d, n_kv, L, size, seed):
