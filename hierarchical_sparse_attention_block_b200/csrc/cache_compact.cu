@@ -141,7 +141,10 @@ __device__ __forceinline__ void sweep(const Array& A, int slice, const int32_t* 
       load(tile[b ^ 1], nxt);
     }
     barrier();  // the rows of the current tile are read by every thread
-    if (*(volatile int*)&dirty) look(j0, tile[b]);
+    // A CTA of the cluster that is ahead may set this flag for its next tile by now, so the threads agree on one
+    // answer (early is fine: the look then finds nothing).  Alone, no one is ahead.
+    const int seen = *(volatile int*)&dirty;
+    if (nc == 1 ? seen : __syncthreads_or(seen)) look(j0, tile[b]);
     const Tile& t = tile[b];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 import cache_reference as ref  # noqa: E402
 from row_ref_cases import limit_of, next_to_the_limit, qscale_of, three_bf16  # noqa: E402
-from test_cache_gpu import check_tree, close, delta, hs, make_inputs, to_gpu  # noqa: E402, F401
+from test_cache_gpu import check_compact, check_tree, close, delta, hs, make_inputs, some_arrays, to_gpu  # noqa: E402, F401
 
 
 def scores_next_to_the_limit(T, H, b, n_kv, d, seed):
@@ -120,3 +120,26 @@ SIZES = [2.0**24, 2.0**27, 2.0**28, 2.0**31, 2.0**34, 1e12, 2.0**70, 2.0**100]
 @pytest.mark.parametrize("T,H,Hk,d", [(2, 2, 2, 64), (8, 4, 2, 128)])
 def test_large_finite_scores(hs, size, T, H, Hk, d):
     check_far(hs, size, T, H, Hk, d, 2000, 1900)
+
+
+@pytest.mark.parametrize("b,n", [(1, 20_000), (1, 4_097), (2, 9_000), (12, 1_100)])
+def test_bad_entries_over_clusters(hs, b, n):
+    """Lists that break the rules first in any tile, where several CTAs sweep a slice together: one fault near each
+    place in turn, faults everywhere, and a list that is bad from its last entry on."""
+    rng = np.random.RandomState(n)
+    n_kv = 2 * n
+    good = np.stack([np.sort(rng.choice(n_kv, n, replace=False)) for _ in range(b)])
+    arrays = some_arrays(b, n_kv, n, ((2, 64), (3,), ()))
+    for at in sorted({0, 1, 255, 256, 511, 512, 1023, 1024, 2047, 2048, 4096, n // 2, n - 2, n - 1}):
+        if at >= n:
+            continue
+        rows = good.copy()
+        rows[rng.randint(b), at] = rng.choice([-1, -7, n_kv, 0, n_kv - 1])
+        check_compact(hs, rows, None, arrays)
+    rows = good.copy()
+    rows[rng.rand(b, n) < 0.01] = -1
+    rows[rng.rand(b, n) < 0.01] = n_kv + 3
+    swap = np.flatnonzero(rng.rand(n - 1) < 0.01)
+    rows[:, swap], rows[:, swap + 1] = rows[:, swap + 1], rows[:, swap].copy()
+    check_compact(hs, rows, None, arrays)
+    check_compact(hs, rows, list(range(b)), arrays)
