@@ -96,21 +96,28 @@ def far_scores(T, H, Hk, d, n_kv, L, size, seed):
     sign = 1.0 - 2.0 * (torch.arange(T) % 2)
     x["q"] = (u * 2.0**a * sign[:, None, None]).expand(1, T, H, d).to(torch.bfloat16).contiguous()
     x["k"] = (u * 2.0**c * level[None, :, None, None]).expand(1, n_kv, Hk, d).to(torch.bfloat16).contiguous()
-    return x
+    return x, sign, level, float((u.double() * u.double()).sum()) * 2.0 ** (a + c) / math.sqrt(d)
 
 
 def check_far(hs, size, T, H, Hk, d, n_kv, L):
     """A score is off by (d + 8) 2^-23 of itself, 2e-5 of the distance of at least half to any other score, so the
     weights are those of the largest scores alone, and these are equal: o carries the roundings of the weights (equal
     ones cancel, 2^-14 for the sums) and of the output, lse the largest score's error."""
-    x = far_scores(T, H, Hk, d, n_kv, L, size, seed=int(math.log2(size)) + T)
+    x, sign, level, unit = far_scores(T, H, Hk, d, n_kv, L, size, seed=int(math.log2(size)) + T)
     p = hs.params(1, T, n_kv, 128, 128, 4, 64, H, Hk, d)
     g = to_gpu(x)
     o, lse = hs.tree_attn(p, g["q"], g["k"], g["v"], g["kv_len"], parent=g["parent"])
-    ro, rl, _, spread, _ = ref.tree_attention(x["q"], x["k"], x["v"], x["kv_len"], x["parent"], 1 / math.sqrt(d))
-    assert float(rl.min()) > size / 4
-    close(o, ro, 2.0**-8 * ro.abs() + 2.0**-13 * spread, "o")
-    close(lse, rl, (d + 8) * 2.0**-23 * rl + 2.0**-22 * rl, "lse")
+    # The definition from the keys' lengths: 64-bit dot products beyond 2^52 no longer tell equal scores from unequal.
+    assert unit > size / 4
+    for i, anc in enumerate(ref.ancestors(x["parent"][0], T)):
+        rows = torch.cat([torch.arange(L), L + torch.tensor(anc)])
+        top = rows[sign[i] * level[rows] == 1.0]
+        assert len(top) >= 12 and float((sign[i] * level[rows]).max()) == 1.0
+        v = x["v"][0, top].double().repeat_interleave(H // Hk, 1)
+        want = v.mean(0)
+        close(o[0, i], want, 2.0**-8 * want.abs() + 2.0**-13 * v.abs().mean(0), "o")
+        z = torch.full((H,), unit + math.log(len(top)), dtype=torch.float64)
+        close(lse[0, i], z, (d + 8) * 2.0**-23 * z + 2.0**-22 * z, "lse")
 
 
 SIZES = [2.0**24, 2.0**27, 2.0**28, 2.0**31, 2.0**34, 1e12, 2.0**70, 2.0**100]
