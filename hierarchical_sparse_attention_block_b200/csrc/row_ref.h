@@ -7,6 +7,8 @@
 #pragma once
 
 #include <float.h>
+#include <stdint.h>
+#include <string.h>
 
 #ifdef __CUDACC__
 #define HISA_HD __host__ __device__ __forceinline__
@@ -33,5 +35,23 @@ HISA_HD bool exceeds(float s, RowRef r) { return s - r.ref > r.limit; }
 
 // log2 of a score's weight.
 HISA_HD float exponent(float s, RowRef r, float qscale) { return (s - r.ref) * qscale; }
+
+// For exponents as one multiply-add, s * c - ref * c: the c to take for qscale.  ref * qscale is off by half an ulp,
+// which all of the row's weights carry as a factor: of no matter up to 2^30 (2^+-32), out of fp32's range beyond.
+// There two scores that differ at all differ by 64 in the log2 domain, so that those equal to the largest alone have a
+// weight, with the power of two at or below qscale as well: and products with that are exact.
+HISA_HD float row_scale(float ref, float qscale) {
+  const float z = ref * qscale;
+  if (z < 1073741824.f && z > -1073741824.f) return qscale;
+#ifdef __CUDA_ARCH__
+  return __uint_as_float(__float_as_uint(qscale) & 0x7F800000u);
+#else
+  uint32_t u;
+  memcpy(&u, &qscale, 4);
+  u &= 0x7F800000u;
+  memcpy(&qscale, &u, 4);
+  return qscale;
+#endif
+}
 
 }  // namespace hisa

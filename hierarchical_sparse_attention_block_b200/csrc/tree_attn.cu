@@ -34,6 +34,7 @@
 // Every wait is bounded (1 s): a timeout sets status bit 1 and the CTA stops.
 #include <math.h>
 
+#include "row_ref.h"
 #include "tree_attn.cuh"
 
 namespace hisa {
@@ -294,8 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid & (kRows - 1);
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128u * (uint32_t)t;
-    const float lim = 8.f / qscale;
-    const float2 qs2 = {qscale, qscale};
+    const float lim = rise_limit(qscale);
     float2* join = reinterpret_cast<float2*>(smem + C::JOIN_OFF);
     bool ok = true;
     int cnt = 0, seg = 0;  // key tiles of this group so far, segments
@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             m_run = tmax;
           }
-          const float nmq = m_run == -INFINITY ? 0.f : -m_run * qscale;
-          const float2 nmq2 = {nmq, nmq};
+          const float m0 = m_run == -INFINITY ? 0.f : m_run, qs = row_scale(m0, qscale), nmq = -m0 * qs;
+          const float2 qs2 = {qs, qs}, nmq2 = {nmq, nmq};
           // the weights of a block over its scores: pairs (2 i, 2 i + 1) in the block's first 16 columns
           float2 ls[2] = {{0.f, 0.f}, {0.f, 0.f}};
           auto weigh = [&](int c4, const uint32_t(&x)[32]) {

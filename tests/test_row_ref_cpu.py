@@ -16,6 +16,7 @@ SHIM = """
 #include "row_ref.h"
 extern "C" {
 float limit_of(float q) { return hisa::rise_limit(q); }
+float scale_of(float ref, float q) { return hisa::row_scale(ref, q); }
 float exponent_of(float s, float ref, float q) { return hisa::exponent(s, {ref, 0.f}, q); }
 // Moves (ref, limit) through a tile as the kernel does; returns how many scores still exceed the reference then.
 int tile(const float* s, int n, float q, float* ref, float* limit, int* moved) {
@@ -44,8 +45,9 @@ def shim(tmp_path_factory):
     subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", "-fPIC", "-shared", "-I", CSRC, str(src), "-o",
                     str(so)], check=True)
     lib = ctypes.CDLL(str(so))
-    lib.limit_of.restype = lib.exponent_of.restype = ctypes.c_float
+    lib.limit_of.restype = lib.scale_of.restype = lib.exponent_of.restype = ctypes.c_float
     lib.limit_of.argtypes = [ctypes.c_float]
+    lib.scale_of.argtypes = [ctypes.c_float] * 2
     lib.exponent_of.argtypes = [ctypes.c_float] * 3
     return lib
 
@@ -104,3 +106,22 @@ def test_every_scale_has_a_finite_limit(shim, q):
     for top in (0.0, 5.0, -3e38, 3e38):  # the first score moves the reference at any scale
         left, ref, _, moved = through(shim, [top], q, f32(0), f32(-np.inf))
         assert left == 0 and moved and ref == f32(top)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_by", [1.0, 1e-6, 1e6])
+def test_one_multiply_add_keeps_every_weight_in_range(shim, d, q_by):
+    """s c - ref c in one rounding: the largest score's exponent stays within 2^5, and beyond 2^30 it is 0 and the next
+    smaller score's below -24, so that nothing else counts in fp32."""
+    q = f32(qscale_of(d) * f32(q_by))
+    rng = np.random.default_rng(d)
+    for size in (1.0, 1e6, 2.0**28, 2.0**29.9, 2.0**30.1, 2.0**31, 1e12, 1e25, 1e31):
+        for _ in range(200):
+            top = f32((1 + rng.random()) * size / np.float64(q) * rng.choice([-1, 1]))
+            c = f32(shim.scale_of(top, q))
+            nm = f32(-top * c)
+            e = fma(top, c, nm)
+            assert abs(e) <= 32
+            if abs(np.float64(top) * np.float64(q)) >= 2.0**30 * (1 + 2.0**-23):
+                assert e == 0 and c <= q < 2 * c
+                assert fma(np.nextafter(top, f32(-np.inf)), c, nm) <= -24
