@@ -487,6 +487,8 @@ def hisa_cache_keep(p, weight, kv_len, budget, keep_idx, kept_len, n_first=0, n_
     torch, call = _torch(), "hisa_cache_keep"
     dev = _device_of(call, "weight", weight)
     i32, b = torch.int32, p.batch
+    if not (0 <= n_first < 1 << 31 and 0 <= n_recent < 1 << 31):  # ctypes would take the low 32 bits
+        _refuse(call, f"n_first {n_first}, n_recent {n_recent}: expected counts of rows")
     at = (_dense(call, dev, "weight", weight, torch.float32, (b, p.n_kv)),
           _dense(call, dev, "kv_len", kv_len, i32, (b,)), budget, n_first, n_recent,
           _dense(call, dev, "keep_idx", keep_idx, i32, (b, budget)),
@@ -501,8 +503,8 @@ def hisa_cache_compact(p, rows, arrays, dst_begin=None, dev_status=None, stream=
     torch, call = _torch(), "hisa_cache_compact"
     dev = _device_of(call, "rows", rows)
     i32, b, n_kv = torch.int32, p.batch, p.n_kv
-    if rows.dim() != 2 or not 1 <= len(arrays) <= MAX_ROW_ARRAYS:
-        _refuse(call, f"expected rows [b][n] and 1 to {MAX_ROW_ARRAYS} arrays, got {tuple(rows.shape)} and "
+    if rows.dim() != 2 or rows.shape[1] > n_kv or not 1 <= len(arrays) <= MAX_ROW_ARRAYS:
+        _refuse(call, f"expected rows [b][n], n <= n_kv, and 1 to {MAX_ROW_ARRAYS} arrays, got {tuple(rows.shape)} and "
                       f"{len(arrays)}")
     n = rows.shape[1]
     given = []
