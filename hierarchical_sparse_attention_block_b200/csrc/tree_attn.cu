@@ -712,6 +712,8 @@ __global__ void __launch_bounds__(kWeighThreads)
 }
 
 int row_tiles(const Shape& s) { return s.n_q * (s.H / s.Hkv) > kRows ? 2 : 1; }
+// Query rows of an item, which are also its rows in the partial results.
+int item_rows(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kFewRows ? kFewRows : row_tiles(s) * kRows; }
 
 // With few query rows the weights come from kept scores: writing and reading those moves 8 bytes a query
 // row and key, reading K again 2 d bytes a KV head and key (8 x 64K rows, one query row a KV head: 490 us
@@ -724,7 +726,7 @@ struct Layout {
 };
 Layout layout(const Shape& s, bool with_weight) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = (size_t)kMaxCtas * 2 * row_tiles(s) * kRows;
+  const size_t rows = (size_t)kMaxCtas * 2 * item_rows(s);
   Layout L;
   L.prefix = 0;
   L.part_o = up((size_t)(s.batch + 2) * sizeof(int64_t));
@@ -787,7 +789,7 @@ cudaError_t launch_tree_attn(const Shape& s, const void* q, const void* k, const
   a.H = s.H;
   a.Hkv = s.Hkv;
   a.qscale = s.scale * kLog2e;
-  const int R = a.T * (s.H / s.Hkv), nt = row_tiles(s), tile_rows = R <= kFewRows ? kFewRows : nt * kRows;
+  const int R = a.T * (s.H / s.Hkv), nt = row_tiles(s), tile_rows = item_rows(s);
   const int64_t most = (int64_t)s.batch * s.Hkv * ((R + tile_rows - 1) / tile_rows) * ((s.n_kv + kRows - 1) / kRows);
   const int ctas = (int)(most < kMaxCtas ? most : kMaxCtas);
   cudaError_t e;

@@ -21,3 +21,15 @@ def test_lists_longer_than_the_cache_are_refused(n):
     with pytest.raises(hs.HisaError) as err:
         hs.hisa_cache_compact(_p(), _OnGpu((2, n), torch.int32), [_OnGpu((2, 512, 4), torch.float32)])
     assert err.value.status == hs.HISA_ERR_INVALID_ARG and "n <= n_kv" in str(err.value)
+
+
+@pytest.mark.parametrize("T,G,rows", [(1, 1, 16), (4, 4, 16), (16, 1, 16), (17, 1, 128), (32, 4, 128), (43, 3, 256),
+                                      (256, 8, 256)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_partial_results_have_the_rows_of_an_item(T, G, rows, d):
+    """Scratch of a call without weights: two partial results for each of 148 CTAs, of 16, 128 or 256 query rows of
+    d + 2 numbers, the lengths' sums, and at most 256 bytes of padding for each of the three."""
+    b = 3
+    need = hs.hisa_tree_attn_workspace_size(_p(batch=b, n_q=T, n_kv=4096, n_heads=2 * G, n_kv_heads=2, d_head=d))
+    least = 148 * 2 * rows * (d + 2) * 4 + 8 * (b + 2)
+    assert least <= need <= least + 3 * 256

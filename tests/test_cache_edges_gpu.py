@@ -192,3 +192,23 @@ def test_bad_entries_over_clusters(hs, b, n):
     rows[:, swap], rows[:, swap + 1] = rows[:, swap + 1], rows[:, swap].copy()
     check_compact(hs, rows, None, arrays)
     check_compact(hs, rows, list(range(b)), arrays)
+
+
+@pytest.mark.parametrize("T,H,Hk,d,n_kv", [(1, 4, 2, 64, 9000), (16, 2, 2, 128, 5000), (17, 2, 2, 128, 5000),
+                                           (64, 4, 2, 64, 3000), (200, 6, 2, 128, 3000)])
+@pytest.mark.parametrize("weigh", [False, True])
+def test_scratch_of_the_stated_size_is_enough(hs, T, H, Hk, d, n_kv, weigh):
+    """Bytes behind the workspace stay as they were, and the result does not depend on what the workspace held."""
+    b = 3
+    g = to_gpu(make_inputs(b, T, H, Hk, d, n_kv, [n_kv - T, n_kv // 3, 0], "tree", seed=T, garbage=False))
+    p = hs.params(b, T, n_kv, 128, 128, 4, 64, H, Hk, d)
+    need = hs.hisa_tree_attn_workspace_size(p, weigh)
+    out = []
+    for fill in (0x5A, 0xFF):  # 0xFF: NaN everywhere
+        block = torch.full((need + 65536,), fill, dtype=torch.uint8, device="cuda")
+        o, lse, w = torch.empty_like(g["q"]), torch.empty(b, T, H, device="cuda"), g["weight"].clone()
+        hs.hisa_tree_attn_fwd(p, g["q"], g["k"], g["v"], g["kv_len"], o, lse, parent=g["parent"],
+                              weight=w if weigh else None, workspace=block[:need])
+        assert bool((block[need:] == fill).all())
+        out.append((o, lse, w))
+    assert all(torch.equal(x, y) for x, y in zip(*out))
