@@ -82,10 +82,14 @@ __device__ __forceinline__ int64_t tile_sum(int64_t L, int T) {
 __device__ __forceinline__ int64_t tiles_of(int64_t sum) { return sum & (((int64_t)1 << 44) - 1); }
 __device__ __forceinline__ int64_t units_of(int64_t sum, int lead) { return tiles_of(sum) + lead * (sum >> 44); }
 
-// The CTA's walk; all NT threads call, two barriers.  lead: units without a tile in front of an item,
-// where a CTA has at least 5 tiles (else none; 3 x 5003 rows, 600 query rows, 7 tiles a CTA: 46 us without
-// them, 42 with).  prefix (nullable, [batch + 2]): CTA 0 writes the units per
-// item of the sequences before each, of all, and the lead; it also flags lengths out of range.
+// The CTA's walk; all NT threads call, two barriers.  lead: units without a tile in front of an item, where the
+// call has a tile for each SM (else none).  us without them and with them, by tiles a CTA, in a replayed graph:
+//   4 x n rows, 16 heads on 4, 32 tokens, d = 128:    0.6: 24.1, 22.9   1.4: 35.2, 29.0   3: 37.2, 31.1   12: 51, 46
+//   4 x n rows, 16 heads on 2, 64 tokens, d = 128:    0.6: 31.0, 33.5   1.4: 47.3, 37.2   3: 51.4, 41.2   12: 78, 63
+//   4 x n rows, 8 heads on 4, one token, d = 64:      0.6: 16.9, 17.2   1.4: 21.0, 19.5   3: 24.9, 23.9   12: 38, 38
+//   received weight, 16 heads on 4, 32 tokens:        0.6: 16.8, 18.6   1.4: 23.3, 20.7   3: 24.3, 22.5   12: 33, 32
+// prefix (nullable, [batch + 2]): CTA 0 writes the units per item of the sequences before each, of all, and the
+// lead; it also flags lengths out of range.
 template <int NT>
 __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch, int per_seq, int lead,
                            WalkShared<NT>& sm, int64_t* prefix, int32_t* status) {
@@ -116,7 +120,7 @@ __device__ Walk walk_begin(const int32_t* kv_len, int64_t n_kv, int T, int batch
     if (w < warp) before_sum += x;
     total_sum += x;
   }
-  if (tiles_of(total_sum) * per_seq < 5 * (int64_t)gridDim.x) lead = 0;
+  if (tiles_of(total_sum) * per_seq < kMaxCtas) lead = 0;
   const int64_t before = units_of(before_sum, lead), total = units_of(total_sum, lead);
   const int64_t units = total * per_seq, ctas = range_ctas(units, gridDim.x);
   const bool busy = blockIdx.x < ctas;

@@ -212,3 +212,14 @@ def test_scratch_of_the_stated_size_is_enough(hs, T, H, Hk, d, n_kv, weigh):
         assert bool((block[need:] == fill).all())
         out.append((o, lse, w))
     assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+@pytest.mark.parametrize("tiles", [147, 149, 210, 444])
+@pytest.mark.parametrize("T,H", [(20, 1), (100, 3), (3, 1), (128, 2)])
+def test_a_tile_or_a_few_for_every_sm(hs, tiles, T, H):
+    """One item, or one a sequence, whose first shares of the work may hold no key tile: attention and weights."""
+    rows = tiles * 128 - T - 50
+    for lens in ([rows], [rows // 3, rows // 2, 0, rows - rows // 3 - rows // 2]):
+        n_kv = max(lens) + T
+        x = make_inputs(len(lens), T, H, 1, 64, n_kv, lens, "tree", seed=T, garbage=False)
+        check_tree(hs, x, H, 1, 64, True)
