@@ -715,10 +715,15 @@ int row_tiles(const Shape& s) { return s.n_q * (s.H / s.Hkv) > kRows ? 2 : 1; }
 // Query rows of an item, which are also its rows in the partial results.
 int item_rows(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kFewRows ? kFewRows : row_tiles(s) * kRows; }
 
-// With few query rows the weights come from kept scores: writing and reading those moves 8 bytes a query
-// row and key, reading K again 2 d bytes a KV head and key (8 x 64K rows, one query row a KV head: 490 us
-// this way, 740 with K read again).
-bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kFewRows; }
+// Up to 8 query rows of a KV head the weights come from kept scores: writing and reading those moves 8 bytes a
+// query row and key, reading K again 2 d bytes a key, and forms the scores again.  us with kept scores and with K
+// read again, in a replayed graph, by query rows:
+//   8 x 32K rows, 4 KV heads, d = 128:    1: 115, 156   4: 122, 155   8: 136, 156   16: 168, 155
+//   2 x 16K rows, 16 KV heads, d = 128:   1: 64, 96     4: 72, 96     8: 82, 96     16: 108, 97
+//   8 x 32K rows, 4 KV heads, d = 64:     1: 99, 121    4: 106, 121   8: 115, 121   16: 135, 121
+//   2 x 16K rows, 16 KV heads, d = 64:    1: 63, 81     4: 74, 81     8: 89, 81     16: 121, 81
+constexpr int kKeptRows = 8;
+bool keeps_scores(const Shape& s) { return s.n_q * (s.H / s.Hkv) <= kKeptRows; }
 int64_t score_stride(const Shape& s) { return (s.n_kv + kRows - 1) / kRows * kRows; }
 
 struct Layout {

@@ -33,3 +33,15 @@ def test_partial_results_have_the_rows_of_an_item(T, G, rows, d):
     need = hs.hisa_tree_attn_workspace_size(_p(batch=b, n_q=T, n_kv=4096, n_heads=2 * G, n_kv_heads=2, d_head=d))
     least = 148 * 2 * rows * (d + 2) * 4 + 8 * (b + 2)
     assert least <= need <= least + 3 * 256
+
+
+@pytest.mark.parametrize("T,G,kept", [(1, 1, True), (8, 1, True), (2, 4, True), (9, 1, False), (4, 4, False)])
+def test_scratch_of_a_call_with_weights(T, G, kept):
+    """Up to 8 query rows a KV head the scores are kept: 4 bytes a query row and key tile row; above, a sum a key and
+    head group at most."""
+    b, n_kv, Hk = 3, 4000, 2
+    p = _p(batch=b, n_q=T, n_kv=n_kv, n_heads=Hk * G, n_kv_heads=Hk, d_head=64)
+    more = hs.hisa_tree_attn_workspace_size(p, True) - hs.hisa_tree_attn_workspace_size(p, False)
+    scores = 4 * b * T * Hk * G * 4096
+    assert (scores <= more <= scores + 4 * b * T * Hk * G + 512) == kept
+    assert kept or more <= 4 * b * n_kv * Hk + 4 * b * T * Hk * G + 512

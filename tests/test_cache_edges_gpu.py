@@ -223,3 +223,10 @@ def test_a_tile_or_a_few_for_every_sm(hs, tiles, T, H):
         n_kv = max(lens) + T
         x = make_inputs(len(lens), T, H, 1, 64, n_kv, lens, "tree", seed=T, garbage=False)
         check_tree(hs, x, H, 1, 64, True)
+
+
+@pytest.mark.parametrize("T,H,Hk", [(7, 1, 1), (8, 1, 1), (9, 1, 1), (4, 4, 2), (3, 6, 2), (1, 16, 2), (2, 10, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_where_scores_are_kept_and_where_not(hs, T, H, Hk, d):
+    x = make_inputs(3, T, H, Hk, d, 700, [700 - T, 128, 5], "tree", seed=T + H)
+    check_tree(hs, x, H, Hk, d, True)
