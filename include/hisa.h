@@ -339,6 +339,14 @@ hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_
  *     (token i follows i - 1; T = 1 is a plain decode step).
  *   Token i sees the context, its ancestors and itself:
  *     V(i) = [0, L) and L + j for j in anc(i) or j = i.
+ * What a call writes shares no bytes with its other arrays (but kept_len with
+ * kv_len).  The context's own values may be anything: a score of +inf or NaN
+ * makes its query rows NaN, a value of V that is not finite makes that column
+ * of the rows that see it not finite.
+ * After an eviction the sequences have lengths of their own: hisa_tree_attn_fwd
+ * takes them (T = 1: a decode step).  hisa_block_pool, hisa_forward and
+ * hisa_forward_cached take one n_kv for all sequences, their stride as well, so
+ * the two-level path does not run over such a cache.
  * A step: append the drafted tokens' rows -> hisa_tree_attn_fwd -> (accept a
  * path) -> hisa_cache_weight for the accepted tokens -> hisa_cache_compact
  * moves their rows to the context's end; once the cache is full,
@@ -352,14 +360,20 @@ hisa_status_t hisa_lse_merge(const void* o_parts, const float* lse_parts, int32_
  * bf16 output; with up to 16 query rows per KV head (T * H / Hk) the weights
  * multiply V to 16 significant bits, with more as bf16 (each output then stays
  * within 2^-8 sum_t softmax_t |v| of the exact one before its own rounding).
+ * Scores may be as large as fp32 holds; what bounds them is their own rounding.
  * weight (nullable) [b][n_kv] fp32: the attention weight each row receives,
  *   a(t) = sum over slots i with t in V(i) and heads h of exp(z(t) - lse[s][i][h]),
  * is added on the context's rows (weight[s][t] += a(t), t < L) and replaces
  * what the drafted rows held (weight[s][t] = a(t), L <= t < L + T; 0 for an
- * empty slot's row); later rows stay as they are.  Where drafted tokens may be
+ * empty slot's row); later rows stay as they are.  It is formed from the fp32
+ * LSE, whose rounding it has: relative 2^-22 |lse|.  Where drafted tokens may be
  * rejected, pass NULL and call hisa_cache_weight for the accepted ones.
  * Workspace: hisa_tree_attn_workspace_size bytes (with_weight: 1 if weight is
- * passed, 0 if not), 16-byte aligned, used by one call at a time. */
+ * passed, 0 if not), 16-byte aligned, used by one call at a time: partial
+ * results (1.2 to 39 MB), and with weight up to 8 query rows per KV head the
+ * scores (4 T H n_kv bytes a sequence, T H / (Hk d) of the K and V rows: an
+ * eighth at the most), above those 4 n_kv bytes a sequence and group of KV
+ * heads, none where one group has all heads. */
 hisa_status_t hisa_tree_attn_workspace_size(const hisa_params_t* params, int32_t with_weight, size_t* bytes);
 hisa_status_t hisa_tree_attn_fwd(const hisa_params_t* params, const void* q, const void* k, const void* v,
                                  const int32_t* kv_len, const int32_t* parent, void* o, float* lse, float* weight,
