@@ -3,13 +3,12 @@
 //
 //   S^T = K Q^T  (128 keys x N),   O^T += V^T P^T  (D x N),   N = 16 >= T H / Hk query rows.
 //
-// The call is bound by the cache's bytes (K and V once): 8 x 64K rows, one query row a KV head, take
-// 421 to 444 us (GPUs differ), 6.5 to 6.8 TB/s.  With the query rows as the M = 128 of the products, as tree_attn.cu has them, one to
-// 16 of 128 rows would be padding (446 us, with weights of 8 bits).  Here the products shrink with N, a
-// thread, which owns a key, forms that key's weights of all rows, and keeping the scores for the weights
-// that the rows receive is a coalesced store.  From 17 rows on the stores of the weights, two bytes at a
-// time, take longer than the tile's bytes (8 x 32K rows, 32 query rows: 150 us this way with N = 32, 129
-// the other).
+// The call is bound by the cache's bytes (K and V once): 8 x 64K rows of different lengths, one query row a KV
+// head, take 421 to 444 us (GPUs differ), 6.5 to 6.8 TB/s.  With the query rows as the M = 128 of the products, as
+// tree_attn.cu has them, one to 16 of 128 rows would be padding (446 us, with weights of 8 bits).  Here the products
+// shrink with N, a thread, which owns a key, forms that key's weights of all rows, and keeping the scores for the
+// weights that the rows receive is a coalesced store.  From 17 rows on the stores of the weights, two bytes at a
+// time, take longer than the tile's bytes (8 x 32K rows, 32 query rows: 150 us this way with N = 32, 129 the other).
 //
 // Work and ring buffers are those of tree_attn.cu (one row tile).  Scores and weights have two buffers,
 // used by the key tiles in turn; the two softmax groups of four warps take half of the query rows each.
@@ -19,8 +18,8 @@
 // barrier, and only where one found it, rarely, reduce the rows' max, rescale and form the weights again (once a
 // tile: after that no score of the tile exceeds it; row_ref.h has the arithmetic).
 // (Starting from the first tile's max instead: 1 x 1K rows, 16 query rows, 18.2 us, 15.7 this way with the
-// sums by halving.)  A row's sum stays a partial sum per thread until the segment's end.  The weights go to shared memory, in the layout of the second product's
-// operand, as two bf16 numbers each (16 significant bits).
+// sums by halving.)  A row's sum stays a partial sum per thread until the segment's end.  The weights go to
+// shared memory, in the layout of the second product's operand, as two bf16 numbers each (16 significant bits).
 // Every wait is bounded (1 s): a timeout sets status bit 1 and the CTA stops.
 #include <math.h>
 
